@@ -28,7 +28,10 @@ EXPORTED = ("m3_ssm_prefill_workspace_bytes", "m3_ssm_prefill", "m3_ssm_decode_s
             "m3_ssm_prefill_backward", "m3_ssm_prefill_backward_ex", "m3_ssm_prefill_backward_plan",
             "m3_ssm_prefill_noalloc",
             "m3_ssm_prefill_plan",
-            "m3_ceiling_mfma", "m3_ceiling_stream")
+            "m3_ceiling_mfma", "m3_ceiling_stream",
+           "m3_linear_prefill_workspace_bytes", "m3_linear_plan", "m3_linear_prefill", "m3_linear_decode_step",
+           "m3_linear_prefill_backward_workspace_bytes", "m3_linear_prefill_backward",
+           "m3_norm_rotate", "m3_norm_rotate_backward_workspace_bytes", "m3_norm_rotate_backward")
 
 # Size of the static workspace of m3_ssm_prefill_noalloc (include/m3_ssm_noalloc.h).
 M3_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -69,6 +72,27 @@ class m3_grads_t(ctypes.Structure):
 class m3_final_grads_t(ctypes.Structure):
     """Incoming gradients of the final carried state (include/m3_ssm_backward.h)."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("h", "phi", "prev_B", "prev_x")]
+
+
+class m3_rows_t(ctypes.Structure):
+    """Rows [token][head][channel] (include/m3_linear.h): strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class m3_linear_shape_t(ctypes.Structure):
+    """Problem size of linear attention (include/m3_linear.h)."""
+    _fields_ = [("batch", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_seqlen", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("v_heads", ctypes.c_int32),
+                ("key_dim", ctypes.c_int32), ("value_dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class m3_rotary_shape_t(ctypes.Structure):
+    """Problem size of the norm and rotation of q and k rows (include/m3_rotary.h)."""
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("pos_int64", ctypes.c_int32), ("halves", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class M3Error(RuntimeError):
@@ -128,6 +152,25 @@ def load():
     lib.m3_ceiling_mfma.restype = ctypes.c_int
     lib.m3_ceiling_stream.argtypes = [ctypes.c_int32, vp, vp, ctypes.c_int64, ctypes.c_int32, vp]
     lib.m3_ceiling_stream.restype = ctypes.c_int
+    lsp, rp = ctypes.POINTER(m3_linear_shape_t), ctypes.POINTER(m3_rows_t)
+    i64, sz = ctypes.c_int64, ctypes.c_size_t
+    for name, args in (
+            ("m3_linear_prefill", [lsp, rp, rp, rp, vp, vp, vp, i64, vp, vp, rp, vp, sz, vp]),
+            ("m3_linear_decode_step", [lsp, rp, rp, rp, vp, vp, i64, vp, rp, vp]),
+            ("m3_linear_prefill_backward", [lsp, rp, rp, rp, vp, vp, vp, rp, vp, rp, rp, rp, vp, vp, sz, vp]),
+            ("m3_linear_plan", [lsp, i64p, i64p])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    qsp = ctypes.POINTER(m3_rotary_shape_t)
+    for name, args in (
+            ("m3_norm_rotate", [qsp, rp, rp, vp, vp, vp, vp, rp, rp, vp]),
+            ("m3_norm_rotate_backward", [qsp, rp, rp, vp, vp, vp, vp, rp, rp, rp, rp, vp, vp, vp, sz, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    for name, arg in (("m3_linear_prefill_workspace_bytes", lsp), ("m3_linear_prefill_backward_workspace_bytes", lsp),
+                      ("m3_norm_rotate_backward_workspace_bytes", qsp)):
+        getattr(lib, name).argtypes = [arg]
+        getattr(lib, name).restype = sz
     lib.m3_status_string.argtypes = [ctypes.c_int]
     lib.m3_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -244,3 +287,46 @@ def m3_ssm_prefill_backward_plan(shape):
     sg, tk = ctypes.c_int32(0), ctypes.c_int64(0)
     rc = int(load().m3_ssm_prefill_backward_plan(ctypes.byref(shape), ctypes.byref(sg), ctypes.byref(tk)))
     return rc, sg.value, tk.value
+
+
+# Linear attention and rotary rows: structures are passed as they are (ctypes
+# takes the address of an instance for a pointer argument), addresses as ints
+# or None.
+
+def m3_linear_prefill_workspace_bytes(shape: m3_linear_shape_t) -> int:
+    return int(load().m3_linear_prefill_workspace_bytes(shape))
+
+
+def m3_linear_prefill_backward_workspace_bytes(shape: m3_linear_shape_t) -> int:
+    return int(load().m3_linear_prefill_backward_workspace_bytes(shape))
+
+
+def m3_linear_plan(shape: m3_linear_shape_t):
+    """(status, tokens per segment of the prompt pass, of the gradients); 0: sequences are not cut."""
+    a, b = ctypes.c_int64(0), ctypes.c_int64(0)
+    rc = int(load().m3_linear_plan(shape, a, b))
+    return rc, a.value, b.value
+
+
+def m3_linear_prefill(*args) -> int:
+    return load().m3_linear_prefill(*args)
+
+
+def m3_linear_decode_step(*args) -> int:
+    return load().m3_linear_decode_step(*args)
+
+
+def m3_linear_prefill_backward(*args) -> int:
+    return load().m3_linear_prefill_backward(*args)
+
+
+def m3_norm_rotate(*args) -> int:
+    return load().m3_norm_rotate(*args)
+
+
+def m3_norm_rotate_backward_workspace_bytes(shape: m3_rotary_shape_t) -> int:
+    return int(load().m3_norm_rotate_backward_workspace_bytes(shape))
+
+
+def m3_norm_rotate_backward(*args) -> int:
+    return load().m3_norm_rotate_backward(*args)

@@ -1,0 +1,549 @@
+// m3_linear.hip -- C ABI of linear attention with a decay for each head
+// (include/m3_linear.h): argument checks, plan, workspace and launch sequence,
+// with the small kernels around the scan of k_linear.hpp: the join of segment
+// states, the sum of a shared row's gradients, the single-token step.
+#include "m3_linear.h"
+#include "k_linear.hpp"
+#include "m3_internal.hpp"
+
+#include <algorithm>
+
+namespace m3 {
+
+// Joins the segment states of a cut sequence in place: slot s holds what the
+// segment before it left from zero and gets the state that segment s starts
+// from; the first slot gets the initial state.  Reading it here only lets the
+// scan's last segment write the final state over it.  blockIdx.x: (sequence,
+// head), blockIdx.y: 1024 entries of the state, blockIdx.z: scan.
+__global__ __launch_bounds__(256) void k_linear_join(const LinParams p) {
+    const LinRole &R = p.role[blockIdx.z];
+    const int64_t b = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int64_t start = lin_start(p, b), next = lin_start(p, b + 1);
+    const int64_t len = next > start ? next - start : 0, n = (len + p.seglen - 1) / p.seglen;
+    if (!R.init && n <= 1) return;
+    const int64_t pool = lin_slot(p.slots, p.nstates, b);
+    if (pool < 0) return;
+    const int64_t area = int64_t(R.dx) * R.dz, e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+    if (e >= area) return;
+    floatx4 s{0.f, 0.f, 0.f, 0.f};
+    if (R.init) {
+        const int64_t at = (pool * p.H + h) * area + e;
+        float v[4];
+        if (R.init16) io<bf16>::load4(static_cast<const bf16 *>(R.init) + at, v);
+        else io<float>::load4(static_cast<const float *>(R.init) + at, v);
+        s = floatx4{v[0], v[1], v[2], v[3]};
+    }
+    float *w = R.seg + (lin_first_slot(p, b) * p.H + h) * area + e;
+    const int64_t step = p.H * area;
+    if (R.init) *reinterpret_cast<floatx4 *>(w) = s;
+    const LinDecay d(p.log_decay[h], double(p.seglen));
+    constexpr int U = 8; // loads in flight
+    for (int64_t i = 1; i < n; i += U) {
+        floatx4 a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < n) a[u] = *reinterpret_cast<const floatx4 *>(w + (i + u) * step);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < n) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[k] = d(s[k]) + a[u][k];
+                *reinterpret_cast<floatx4 *>(w + (i + u) * step) = s;
+            }
+    }
+}
+
+// Gradient rows that several heads share: the heads' parts [token][H][dim]
+// fp32, summed in the heads' order and rounded once; zero for tokens outside
+// every sequence.
+struct LinSum {
+    const float *part;
+    void *out;
+    int64_t ot, oh;
+    int32_t heads, group, dim; // rows of out, heads per row
+};
+struct LinSums {
+    LinSum s[3];
+    int32_t n;
+    LinParams seq; // sequences only
+};
+
+template <typename IO>
+__global__ __launch_bounds__(256) void k_linear_sum(const LinSums p) {
+    const LinSum &s = p.s[blockIdx.y];
+    const int u = s.dim / 8;
+    const int64_t n = p.seq.tokens * s.heads * u;
+    const int64_t lo = lin_start(p.seq, 0), hi = lin_start(p.seq, p.seq.batch);
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int c = int(i % u) * 8, r = int(i / u % s.heads);
+        const int64_t t = i / (int64_t(u) * s.heads);
+        float a[8] = {};
+        if (t >= lo && t < hi) {
+            const float *q = s.part + ((t * s.heads + r) * s.group) * s.dim + c;
+            for (int j = 0; j < s.group; ++j) {
+                float v[8];
+                io<float>::load8(q + int64_t(j) * s.dim, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a[k] += v[k];
+            }
+        }
+        IO *o = static_cast<IO *>(s.out) + t * s.ot + r * s.oh + c;
+        io<IO>::store4(o, a);
+        io<IO>::store4(o + 4, a + 4);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Single-token step.  S <- g S + k v^T and o = scale q^T S over one state of
+// Dk x Dv entries per sequence and head: bound by reading and writing it.  A
+// workgroup takes W columns of one state, four columns per lane in rows of
+// W / 4 lanes, and holds all its rows in registers: every load is issued before
+// the first is used.
+// ---------------------------------------------------------------------------
+struct LinStepParams {
+    const void *q, *k, *v;
+    void *o, *state;
+    int64_t qt, qh, kt, kh, vt, vh, ot, oh;
+    int32_t qg, kg, vg, H, dk, dv, slices;
+    int64_t batch, nstates;
+    const int32_t *slots;
+    const float *log_decay;
+    float scale;
+};
+
+template <typename IO, typename ST, int W>
+__global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
+    constexpr int L = W / 4, RP = 256 / L, NP = 128 / RP; // lanes per row, rows per pass, passes
+    __shared__ float part[4][W];
+    int64_t id = blockIdx.x;
+    const int slice = int(id % p.slices);
+    id /= p.slices;
+    const int h = int(id % p.H);
+    const int64_t b = id / p.H;
+    const int tid = threadIdx.x, c = slice * W + tid % L * 4, r0 = tid / L;
+    const bool in = c < p.dv;
+    IO *o = static_cast<IO *>(p.o) + b * p.ot + h * p.oh;
+
+    int64_t slot = b;
+    if (p.slots) {
+        slot = p.slots[b];
+        if (slot < 0 || slot >= p.nstates) return;
+    }
+    ST *st = static_cast<ST *>(p.state) + (slot * p.H + h) * p.dk * p.dv + c;
+    typename io4<ST>::raw raw[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        if (in && r0 + i * RP < p.dk) raw[i] = io4<ST>::load(st + (r0 + i * RP) * p.dv);
+    const IO *q = static_cast<const IO *>(p.q) + b * p.qt + (h / p.qg) * p.qh;
+    const IO *k = static_cast<const IO *>(p.k) + b * p.kt + (h / p.kg) * p.kh;
+    float qv[NP], kv[NP], v[4] = {};
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        qv[i] = kv[i] = 0.f;
+        if (r0 + i * RP < p.dk) {
+            qv[i] = io<IO>::get(q + r0 + i * RP);
+            kv[i] = io<IO>::get(k + r0 + i * RP);
+        }
+    }
+    if (in) io<IO>::load4(static_cast<const IO *>(p.v) + b * p.vt + (h / p.vg) * p.vh + c, v);
+    if (p.slots && lin_slot(p.slots, p.nstates, b) == kSlotTaken) {
+        if (tid < L && in)
+            for (int j = 0; j < 4; ++j) io<IO>::put(o + c + j, __builtin_nanf(""));
+        return;
+    }
+    const LinDecay d(p.log_decay[h], 1.0);
+    float a[4] = {};
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        if (in && r0 + i * RP < p.dk) {
+            float s[4];
+            io4<ST>::unpack(raw[i], s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[j] = fmaf(kv[i], v[j], d(s[j]));
+                a[j] = fmaf(qv[i], s[j], a[j]);
+            }
+            io<ST>::store4(st + (r0 + i * RP) * p.dv, s);
+        }
+    // rows of one wave, then the four waves
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int m = L; m < 64; m <<= 1) a[j] += __shfl_xor(a[j], m);
+    if (tid % 64 < L)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[tid / 64][tid % 64 * 4 + j] = a[j];
+    __syncthreads();
+    if (tid < L && in) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = p.scale * ((part[0][tid * 4 + j] + part[1][tid * 4 + j]) + (part[2][tid * 4 + j] + part[3][tid * 4 + j]));
+        io<IO>::store4(o + c, a);
+    }
+}
+
+template <typename IO, typename ST>
+hipError_t launch_linear_step(LinStepParams &p, hipStream_t s) {
+    const bool wide = p.batch * p.H * ((p.dv + 63) / 64) >= 1024;
+    p.slices = wide ? (p.dv + 63) / 64 : (p.dv + 31) / 32;
+    const dim3 grid(unsigned(p.batch * p.H * p.slices));
+    if (wide) hipLaunchKernelGGL((k_linear_step<IO, ST, 64>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_linear_step<IO, ST, 32>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+} // namespace m3
+
+namespace {
+
+using m3::LinParams;
+using m3::LinRole;
+
+constexpr size_t kAlign = 256;
+size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int32_t heads(const m3_linear_shape_t *s) { return std::max(s->q_heads, std::max(s->k_heads, s->v_heads)); }
+
+m3_status_t check_shape(const m3_linear_shape_t *s, bool decode) {
+    if (!s) return M3_ERR_INVALID_ARGUMENT;
+    if (s->io_dtype != M3_DTYPE_F32 && s->io_dtype != M3_DTYPE_BF16) return M3_ERR_INVALID_ARGUMENT;
+    if (s->state_dtype != M3_DTYPE_F32 && s->state_dtype != M3_DTYPE_BF16) return M3_ERR_INVALID_ARGUMENT;
+    if (s->batch < 1 || s->q_heads < 1 || s->k_heads < 1 || s->v_heads < 1 || s->key_dim < 1 || s->value_dim < 1)
+        return M3_ERR_INVALID_ARGUMENT;
+    if (!decode && (s->tokens < 0 || s->max_seqlen < 0)) return M3_ERR_INVALID_ARGUMENT;
+    const int32_t H = heads(s);
+    if (H % s->q_heads || H % s->k_heads || H % s->v_heads) return M3_ERR_INVALID_ARGUMENT;
+    if (s->key_dim % 8 || s->value_dim % 8 || s->key_dim > 128 || s->value_dim > 128) return M3_ERR_UNSUPPORTED;
+    // counts of sequences and tokens are indexed in 32 bits (cu_seqlens, slots), workgroups too
+    if (s->batch > (int64_t(1) << 31) - 2 || H > (1 << 20)) return M3_ERR_UNSUPPORTED;
+    if (!decode && s->tokens > (int64_t(1) << 31) - 1) return M3_ERR_UNSUPPORTED;
+    if (double(s->batch) * H * 6 * (decode ? 1 : 1 + double(s->tokens) / s->batch / 256) > 2147483647.0) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+bool strides_ok(const m3_rows_t *r) {
+    return r->token_stride >= 0 && r->head_stride >= 0 && r->token_stride < (int64_t(1) << 24) &&
+           r->head_stride < (int64_t(1) << 40) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+// Rows to read.  Without a row the pointer is not looked at.
+bool rows_ok(const m3_rows_t *r, int64_t tokens) {
+    if (!r) return false;
+    return tokens == 0 || (r->data && aligned16(r->data) && strides_ok(r));
+}
+// Rows to write: no two may overlap, whichever axis is the outer one.
+bool out_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim) {
+    if (!rows_ok(r, tokens)) return false;
+    if (tokens == 0) return true;
+    const int64_t t = r->token_stride, h = r->head_stride;
+    const bool by_token = (tokens == 1 || t >= (heads - 1) * h + dim) && (heads == 1 || h >= dim);
+    const bool by_head = (heads == 1 || h >= (tokens - 1) * t + dim) && (tokens == 1 || t >= dim);
+    return by_token || by_head;
+}
+
+// Columns of z a workgroup takes: fp32 I/O holds three planes of everything.
+int z_tile(int dz, bool f32) { return f32 ? std::min(m3::lin_tile(dz), 64) : m3::lin_tile(dz); }
+
+// Tokens per segment (0: sequences are not cut) for `scans` scans over `columns`
+// column tiles in one launch.
+int64_t segment(const m3_linear_shape_t *s, int scans, int columns) {
+    const int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
+    const int64_t per = int64_t(heads(s)) * scans * columns;
+    if (s->batch * per >= 512 || longest <= 256) return 0;
+    int64_t L = (s->tokens * per / 1024 + 63) / 64 * 64;
+    L = std::max<int64_t>(256, std::min<int64_t>(L, 4096));
+    return longest > L ? L : 0;
+}
+int64_t segment_slots(const m3_linear_shape_t *s, int64_t L) { return L ? s->tokens / L + s->batch : s->batch; }
+
+struct Layout {
+    int64_t L, slots;
+    size_t seg_f, seg_b, part[3], total; // byte offsets: segment states forwards, backwards, the parts of gradients
+};
+Layout prefill_layout(const m3_linear_shape_t *s) {
+    Layout w{};
+    const bool f32 = s->io_dtype == M3_DTYPE_F32;
+    const int zt = z_tile(s->value_dim, f32);
+    w.L = segment(s, 1, (s->value_dim + zt - 1) / zt);
+    w.slots = segment_slots(s, w.L);
+    if (w.L) w.total = round_up(size_t(w.slots) * heads(s) * s->key_dim * s->value_dim * 4);
+    w.total = std::max(w.total, kAlign);
+    return w;
+}
+Layout backward_layout(const m3_linear_shape_t *s) {
+    Layout w{};
+    const int32_t H = heads(s);
+    w.L = segment(s, 3, 1);
+    w.slots = segment_slots(s, w.L);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += round_up(bytes);
+        return o;
+    };
+    if (w.L) {
+        const size_t n = size_t(w.slots) * H * s->key_dim * s->value_dim * 4;
+        w.seg_f = take(n);
+        w.seg_b = take(n);
+    }
+    const int32_t hs[3] = {s->q_heads, s->k_heads, s->v_heads}, ds[3] = {s->key_dim, s->key_dim, s->value_dim};
+    for (int i = 0; i < 3; ++i)
+        if (hs[i] < H) w.part[i] = take(size_t(s->tokens) * H * ds[i] * 4);
+    w.total = std::max(at, kAlign);
+    return w;
+}
+
+// Launches the scans p.role[0 .. n-1], which share their tile sizes.
+hipError_t launch_scan(LinParams p, bool f32, bool out, hipStream_t st) {
+    const int dx = m3::lin_tile(p.role[0].dx), dz = z_tile(p.role[0].dz, f32);
+    p.ztiles = (p.role[0].dz + dz - 1) / dz;
+    for (int i = 1; i < p.nroles; ++i) p.ztiles = std::max(p.ztiles, (p.role[i].dz + dz - 1) / dz);
+    p.nwork = p.nseg * p.H * p.ztiles * p.nroles;
+    switch (dx) {
+    case 32: return f32 ? m3::launch_linear_f32_32(p, dz, out, st) : m3::launch_linear_bf16_32(p, dz, out, st);
+    case 64: return f32 ? m3::launch_linear_f32_64(p, dz, out, st) : m3::launch_linear_bf16_64(p, dz, out, st);
+    case 128: return f32 ? m3::launch_linear_f32_128(p, dz, out, st) : m3::launch_linear_bf16_128(p, dz, out, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+// The scans in as few launches as their tile sizes allow.
+hipError_t launch_scans(const LinParams &all, int n, bool f32, bool out, hipStream_t st) {
+    bool done[3] = {};
+    for (int i = 0; i < n; ++i) {
+        if (done[i]) continue;
+        LinParams p = all;
+        p.nroles = 0;
+        for (int j = i; j < n; ++j)
+            if (!done[j] && m3::lin_tile(all.role[j].dx) == m3::lin_tile(all.role[i].dx) &&
+                z_tile(all.role[j].dz, f32) == z_tile(all.role[i].dz, f32)) {
+                p.role[p.nroles++] = all.role[j];
+                done[j] = true;
+            }
+        const hipError_t e = launch_scan(p, f32, out, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_join(LinParams p, int n, hipStream_t st) {
+    p.nroles = n;
+    const int64_t area = int64_t(p.role[0].dx) * p.role[0].dz;
+    hipLaunchKernelGGL(m3::k_linear_join, dim3(unsigned(p.batch * p.H), unsigned((area + 1023) / 1024), unsigned(n)),
+                       dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+// One operand of a scan.
+struct Rows {
+    const m3_rows_t *r;
+    int32_t heads;
+};
+void set_x(LinRole &R, const Rows &a, int32_t H) { R.x = a.r->data; R.xt = a.r->token_stride; R.xh = a.r->head_stride; R.xg = H / a.heads; }
+void set_y(LinRole &R, const Rows &a, int32_t H) { R.y = a.r->data; R.yt = a.r->token_stride; R.yh = a.r->head_stride; R.yg = H / a.heads; }
+void set_z(LinRole &R, const Rows &a, int32_t H) { R.z = a.r->data; R.zt = a.r->token_stride; R.zh = a.r->head_stride; R.zg = H / a.heads; }
+
+LinParams sequences(const m3_linear_shape_t *s, const int32_t *cu, const int32_t *slots, int64_t nstates, const float *ld,
+                    const Layout &w) {
+    LinParams p{};
+    p.H = heads(s);
+    p.ztiles = 1;
+    p.batch = s->batch;
+    p.tokens = s->tokens;
+    p.cu = cu;
+    p.slots = slots;
+    p.nstates = nstates;
+    p.log_decay = ld;
+    p.seglen = w.L;
+    p.nseg = w.slots;
+    return p;
+}
+
+m3_status_t check_sequences(const m3_linear_shape_t *s, const float *ld, const int32_t *cu, const int32_t *slots,
+                            int64_t nstates, bool states) {
+    if (!ld || (reinterpret_cast<uintptr_t>(ld) & 3)) return M3_ERR_INVALID_ARGUMENT;
+    if (cu && (reinterpret_cast<uintptr_t>(cu) & 3)) return M3_ERR_INVALID_ARGUMENT;
+    if (slots && (reinterpret_cast<uintptr_t>(slots) & 3)) return M3_ERR_INVALID_ARGUMENT;
+    if (!cu && s->tokens % s->batch) return M3_ERR_INVALID_ARGUMENT;
+    if (nstates < 0 || (states && !slots && nstates < s->batch)) return M3_ERR_INVALID_ARGUMENT;
+    return M3_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t m3_linear_prefill_workspace_bytes(const m3_linear_shape_t *shape) {
+    return check_shape(shape, false) == M3_OK ? prefill_layout(shape).total : 0;
+}
+
+size_t m3_linear_prefill_backward_workspace_bytes(const m3_linear_shape_t *shape) {
+    return check_shape(shape, false) == M3_OK ? backward_layout(shape).total : 0;
+}
+
+m3_status_t m3_linear_plan(const m3_linear_shape_t *shape, int64_t *prefill_segment, int64_t *backward_segment) {
+    const m3_status_t sc = check_shape(shape, false);
+    if (sc != M3_OK) return sc;
+    if (prefill_segment) *prefill_segment = prefill_layout(shape).L;
+    if (backward_segment) *backward_segment = backward_layout(shape).L;
+    return M3_OK;
+}
+
+m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
+                              const m3_rows_t *v, const float *log_decay, const int32_t *cu_seqlens,
+                              const int32_t *slots, int64_t nstates, const void *init, void *final_state,
+                              const m3_rows_t *o, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    m3_status_t sc = check_shape(shape, false);
+    if (sc != M3_OK) return sc;
+    const int32_t H = heads(shape);
+    if (!rows_ok(q, shape->tokens) || !rows_ok(k, shape->tokens) || !rows_ok(v, shape->tokens) ||
+        !out_ok(o, shape->tokens, H, shape->value_dim))
+        return M3_ERR_INVALID_ARGUMENT;
+    sc = check_sequences(shape, log_decay, cu_seqlens, slots, nstates, init || final_state);
+    if (sc != M3_OK) return sc;
+    if (!aligned16(init) || !aligned16(final_state)) return M3_ERR_INVALID_ARGUMENT;
+    const Layout w = prefill_layout(shape);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return M3_ERR_WORKSPACE;
+
+    LinParams p = sequences(shape, cu_seqlens, slots, nstates, log_decay, w);
+    LinRole &R = p.role[0];
+    set_x(R, {q, shape->q_heads}, H);
+    set_y(R, {k, shape->k_heads}, H);
+    set_z(R, {v, shape->v_heads}, H);
+    R.out = o->data;
+    R.ot = o->token_stride;
+    R.oh = o->head_stride;
+    R.dx = shape->key_dim;
+    R.dz = shape->value_dim;
+    R.a_in = R.a_init = shape->scale;
+    R.a_state = 1.f;
+    R.init = init;
+    R.fin = final_state;
+    R.init16 = R.fin16 = shape->state_dtype == M3_DTYPE_BF16;
+    R.sm = R.dz;
+    R.sn = 1;
+    R.seg = static_cast<float *>(workspace);
+    const bool f32 = shape->io_dtype == M3_DTYPE_F32;
+    if (w.L) {
+        if (launch_scans(p, 1, f32, false, stream) != hipSuccess) return M3_ERR_HIP;
+        if (launch_join(p, 1, stream) != hipSuccess) return M3_ERR_HIP;
+    }
+    return launch_scans(p, 1, f32, true, stream) == hipSuccess ? M3_OK : M3_ERR_HIP;
+}
+
+m3_status_t m3_linear_decode_step(const m3_linear_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
+                                  const m3_rows_t *v, const float *log_decay, const int32_t *slots, int64_t nstates,
+                                  void *state, const m3_rows_t *o, hipStream_t stream) {
+    const m3_status_t sc = check_shape(shape, true);
+    if (sc != M3_OK) return sc;
+    const int32_t H = heads(shape);
+    if (!rows_ok(q, shape->batch) || !rows_ok(k, shape->batch) || !rows_ok(v, shape->batch) ||
+        !out_ok(o, shape->batch, H, shape->value_dim))
+        return M3_ERR_INVALID_ARGUMENT;
+    if (!log_decay || (reinterpret_cast<uintptr_t>(log_decay) & 3) || (reinterpret_cast<uintptr_t>(slots) & 3))
+        return M3_ERR_INVALID_ARGUMENT;
+    if (!state || !aligned16(state) || nstates < 0 || (!slots && nstates < shape->batch)) return M3_ERR_INVALID_ARGUMENT;
+    m3::LinStepParams p{};
+    p.q = q->data; p.qt = q->token_stride; p.qh = q->head_stride; p.qg = H / shape->q_heads;
+    p.k = k->data; p.kt = k->token_stride; p.kh = k->head_stride; p.kg = H / shape->k_heads;
+    p.v = v->data; p.vt = v->token_stride; p.vh = v->head_stride; p.vg = H / shape->v_heads;
+    p.o = o->data; p.ot = o->token_stride; p.oh = o->head_stride;
+    p.state = state;
+    p.H = H;
+    p.dk = shape->key_dim;
+    p.dv = shape->value_dim;
+    p.batch = shape->batch;
+    p.nstates = nstates;
+    p.slots = slots;
+    p.log_decay = log_decay;
+    p.scale = shape->scale;
+    const bool f32 = shape->io_dtype == M3_DTYPE_F32, s16 = shape->state_dtype == M3_DTYPE_BF16;
+    const hipError_t e = f32 ? (s16 ? m3::launch_linear_step<float, m3::bf16>(p, stream) : m3::launch_linear_step<float, float>(p, stream))
+                             : (s16 ? m3::launch_linear_step<m3::bf16, m3::bf16>(p, stream) : m3::launch_linear_step<m3::bf16, float>(p, stream));
+    return e == hipSuccess ? M3_OK : M3_ERR_HIP;
+}
+
+m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
+                                       const m3_rows_t *v, const float *log_decay, const int32_t *cu_seqlens,
+                                       const void *init, const m3_rows_t *go, const float *gfinal,
+                                       const m3_rows_t *gq, const m3_rows_t *gk, const m3_rows_t *gv, float *ginit,
+                                       void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    m3_status_t sc = check_shape(shape, false);
+    if (sc != M3_OK) return sc;
+    const int32_t H = heads(shape), dk = shape->key_dim, dv = shape->value_dim;
+    const int64_t T = shape->tokens;
+    if (!rows_ok(q, T) || !rows_ok(k, T) || !rows_ok(v, T) || !rows_ok(go, T) || !out_ok(gq, T, shape->q_heads, dk) ||
+        !out_ok(gk, T, shape->k_heads, dk) || !out_ok(gv, T, shape->v_heads, dv))
+        return M3_ERR_INVALID_ARGUMENT;
+    sc = check_sequences(shape, log_decay, cu_seqlens, nullptr, shape->batch, true);
+    if (sc != M3_OK) return sc;
+    if (!aligned16(init) || !aligned16(gfinal) || !aligned16(ginit)) return M3_ERR_INVALID_ARGUMENT;
+    const Layout w = backward_layout(shape);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return M3_ERR_WORKSPACE;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+
+    LinParams p = sequences(shape, cu_seqlens, nullptr, shape->batch, log_decay, w);
+    p.tail = cu_seqlens ? 16 : 0;
+    const Rows rq{q, shape->q_heads}, rk{k, shape->k_heads}, rv{v, shape->v_heads}, rg{go, H};
+    const Rows x[3] = {rg, rv, rk}, y[3] = {rv, rg, rq}, z[3] = {rk, rq, rg};
+    const m3_rows_t *out[3] = {gq, gk, gv};
+    const int32_t out_heads[3] = {shape->q_heads, shape->k_heads, shape->v_heads};
+    m3::LinSums sums{};
+    for (int i = 0; i < 3; ++i) {
+        LinRole &R = p.role[i];
+        set_x(R, x[i], H);
+        set_y(R, y[i], H);
+        set_z(R, z[i], H);
+        R.dx = i < 2 ? dv : dk;
+        R.dz = i < 2 ? dk : dv;
+        if (out_heads[i] < H) {
+            R.out = ws + w.part[i];
+            R.out32 = 1;
+            R.ot = int64_t(H) * R.dz;
+            R.oh = R.dz;
+            sums.s[sums.n++] = {static_cast<const float *>(R.out), out[i]->data, out[i]->token_stride, out[i]->head_stride,
+                                out_heads[i], H / out_heads[i], R.dz};
+        } else {
+            R.out = out[i]->data;
+            R.ot = out[i]->token_stride;
+            R.oh = out[i]->head_stride;
+        }
+        R.rev = i > 0;
+        R.a_in = shape->scale;
+        R.a_init = i > 0 ? 1.f : shape->scale;
+        R.a_state = i > 0 ? shape->scale : 1.f;
+        R.init = i > 0 ? static_cast<const void *>(gfinal) : init;
+        R.init16 = i == 0 && shape->state_dtype == M3_DTYPE_BF16;
+        // the pools hold [key][value]; dq and dk scan with the transposed state
+        R.sm = i < 2 ? 1 : dv;
+        R.sn = i < 2 ? dv : 1;
+        R.seg = reinterpret_cast<float *>(ws + (i > 0 ? w.seg_b : w.seg_f));
+        if (i == 2) R.fin = ginit;
+    }
+    const bool f32 = shape->io_dtype == M3_DTYPE_F32;
+    if (w.L) {
+        // the state forwards (of k and v) and its gradient backwards (of q and go), as [key][value]
+        LinParams a = p;
+        a.role[0] = p.role[2];
+        set_y(a.role[0], rk, H);
+        set_z(a.role[0], rv, H);
+        a.role[0].rev = 0;
+        a.role[0].a_state = 1.f;
+        a.role[0].seg = p.role[0].seg;
+        a.role[0].init = p.role[0].init;
+        a.role[0].init16 = p.role[0].init16;
+        a.role[1] = p.role[2];
+        if (launch_scans(a, 2, f32, false, stream) != hipSuccess) return M3_ERR_HIP;
+        if (launch_join(a, 2, stream) != hipSuccess) return M3_ERR_HIP;
+    }
+    if (launch_scans(p, 3, f32, true, stream) != hipSuccess) return M3_ERR_HIP;
+    if (sums.n && T > 0) {
+        sums.seq = p;
+        const dim3 grid(2048, unsigned(sums.n));
+        if (f32) hipLaunchKernelGGL(m3::k_linear_sum<float>, grid, dim3(256), 0, stream, sums);
+        else hipLaunchKernelGGL(m3::k_linear_sum<m3::bf16>, grid, dim3(256), 0, stream, sums);
+        if (hipGetLastError() != hipSuccess) return M3_ERR_HIP;
+    }
+    return M3_OK;
+}
+
+} // extern "C"

@@ -1,0 +1,426 @@
+// m3_rotary.hip -- the norm of queries and keys for each head with the position
+// rotation in the same pass, and its gradients (include/m3_rotary.h).
+//
+// A row of dim channels lies over LPR lanes, eight channels a lane, so a wave
+// takes 64 / LPR rows at once, and the mean of squares is a sum over LPR lanes.
+// A lane's channels are four rotation pairs whichever way the pairs lie, and
+// they are the same pairs in every row: a wave takes up to kRows sets of rows
+// of one token and forms the four angles' sine and cosine once for all of
+// them.  Bound by reading and writing the rows.
+#include "m3_rotary.h"
+#include "m3_device.hpp"
+
+#include <algorithm>
+
+namespace m3 {
+
+constexpr int kRT = 256;   // threads, four waves
+constexpr int kRows = 4;   // row sets per wave and token
+
+struct RotRows {
+    const void *x, *g;     // input rows; upstream gradient (backward)
+    void *out;
+    int64_t xt, xh, gt, gh, ot, oh;
+    const float *w;
+    int32_t heads, items;  // items: groups of kRows row sets
+};
+struct RotParams {
+    RotRows r[2];          // q, k
+    int64_t tokens;
+    int32_t dim, rot, axes, pos64, halves, norm;
+    float eps;
+    const void *pos;
+    const float *freq;
+    float *part;           // backward: [workgroup][2][dim] partial gradients of the weights
+};
+
+// The channels and angles of one lane.
+struct RotLane {
+    int c0, c1;            // two runs of four channels
+    bool in, turn, halves; // channels within the row; turned; pairs across the runs
+    float cs[4], sn[4];
+
+    __device__ __forceinline__ RotLane(const RotParams &p, int unit) {
+        in = unit * 8 < p.dim;
+        turn = unit * 8 < p.rot;
+        halves = p.halves != 0;
+        c0 = halves && turn ? 4 * unit : 8 * unit;
+        c1 = halves && turn ? p.rot / 2 + 4 * unit : 8 * unit + 4;
+    }
+    // Angles as fractions of a turn: far positions times fast frequencies lose
+    // all of fp32.  position * frequency and its product with 1 / 2 pi are taken
+    // as fp64 values with their remainders (fma), so that whole turns drop out
+    // exactly and the rest is good to 2^-50 of a turn up to positions of 2^53.
+    // It goes to the hardware's sine and cosine of turns (at most 1.3e-7 off).
+    __device__ __forceinline__ void angles(const RotParams &p, int unit, int64_t token) {
+#pragma clang fp contract(off) // u must be the rounded product where its remainder is added
+        if (!turn) return;
+        constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57; // 1 / 2 pi = kHi + kLo
+        double a[4] = {};
+        for (int x = 0; x < p.axes; ++x) {
+            const int64_t i = x * p.tokens + token;
+            const double t = p.pos64 ? double(static_cast<const int64_t *>(p.pos)[i]) : double(static_cast<const int32_t *>(p.pos)[i]);
+            const float4 f = *reinterpret_cast<const float4 *>(p.freq + x * (p.rot / 2) + 4 * unit);
+            const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const double m = t * double(fs[c]), u = m * kHi;
+                const double rest = fma(m, kHi, -u) + fma(m, kLo, fma(t, double(fs[c]), -m) * kHi);
+                a[c] += (u - rint(u)) + rest;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float f = float(a[c] - rint(a[c]));
+            sn[c] = __builtin_amdgcn_sinf(f);
+            cs[c] = __builtin_amdgcn_cosf(f);
+        }
+    }
+    // Turns the eight channels by the angles, or back by them.
+    __device__ __forceinline__ void rotate(float v[8], bool back) const {
+        if (!turn) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int a = halves ? i : 2 * i, b = halves ? 4 + i : 2 * i + 1;
+            const float s = back ? -sn[i] : sn[i], u = v[a], w = v[b];
+            v[a] = u * cs[i] - w * s;
+            v[b] = u * s + w * cs[i];
+        }
+    }
+};
+
+template <typename IO>
+struct RotRaw {
+    typename io4<IO>::raw a, b;
+    __device__ __forceinline__ void load(const IO *p, const RotLane &l) { a = io4<IO>::load(p + l.c0); b = io4<IO>::load(p + l.c1); }
+    __device__ __forceinline__ void unpack(float v[8]) const { io4<IO>::unpack(a, v); io4<IO>::unpack(b, v + 4); }
+};
+
+// One token's item j: row sets of q, then of k.
+__device__ __forceinline__ const RotRows &rot_rows(const RotParams &p, int &j) {
+    if (j < p.r[0].items) return p.r[0];
+    j -= p.r[0].items;
+    return p.r[1];
+}
+
+template <typename IO, int LPR>
+__global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
+    constexpr int RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63, unit = lane % LPR, sub = lane / LPR;
+    const int items = p.r[0].items + p.r[1].items;
+    const int64_t item = int64_t(blockIdx.x) * (kRT / 64) + (threadIdx.x >> 6), token = item / items;
+    if (token >= p.tokens) return;
+    int j = int(item % items);
+    const bool is_q = j < p.r[0].items;
+    if (!is_q) j -= p.r[0].items;
+    const RotRows R = is_q ? p.r[0] : p.r[1];
+    RotLane l(p, unit);
+    const int h0 = j * kRows * RPW + sub;
+    const IO *x = static_cast<const IO *>(R.x) + token * R.xt;
+    IO *o = static_cast<IO *>(R.out) + token * R.ot;
+    RotRaw<IO> raw[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        if (l.in && h0 + i * RPW < R.heads) raw[i].load(x + (h0 + i * RPW) * R.xh, l);
+    float w[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) w[c] = 1.f;
+    if (R.w && l.in) {
+        io<float>::load4(R.w + l.c0, w);
+        io<float>::load4(R.w + l.c1, w + 4);
+    }
+    l.angles(p, unit, token);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const bool on = l.in && h0 + i * RPW < R.heads;
+        float v[8] = {};
+        if (on) raw[i].unpack(v);
+        if (p.norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
+            const float r = rsqrtf(row_sum<LPR>(ss) / float(p.dim) + p.eps);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] *= r * w[c];
+        }
+        l.rotate(v, false);
+        if (on) {
+            io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c0, v);
+            io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c1, v + 4);
+        }
+    }
+}
+
+// With n = w r x, r = 1 / sqrt(mean x^2 + eps) and gn the gradient turned back:
+//     dw = sum gn r x,    dx = r w gn - (r^3 / dim) x sum(x w gn).
+// Workgroups walk the items with a fixed stride and keep their share of dw in
+// registers; k_norm_rotate_sum adds the shares in a fixed order.
+template <typename IO, int LPR>
+__global__ __launch_bounds__(kRT) void k_norm_rotate_backward(const RotParams p) {
+    constexpr int RPW = 64 / LPR, NW = kRT / 64;
+    __shared__ float part[NW][LPR * 8];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, unit = lane % LPR, sub = lane / LPR;
+    RotLane l(p, unit);
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const RotRows R = kind ? p.r[1] : p.r[0];
+        if (R.items == 0) continue;
+        float w[8], dw[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = 1.f, dw[c] = 0.f;
+        if (R.w && l.in) {
+            io<float>::load4(R.w + l.c0, w);
+            io<float>::load4(R.w + l.c1, w + 4);
+        }
+        for (int64_t item = int64_t(blockIdx.x) * NW + wave; item < p.tokens * R.items; item += int64_t(gridDim.x) * NW) {
+            const int64_t token = item / R.items;
+            const int h0 = int(item % R.items) * kRows * RPW + sub;
+            const IO *x = static_cast<const IO *>(R.x) + token * R.xt;
+            const IO *g = static_cast<const IO *>(R.g) + token * R.gt;
+            IO *o = static_cast<IO *>(R.out) + token * R.ot;
+            RotRaw<IO> rx[kRows], rg[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (l.in && h0 + i * RPW < R.heads) {
+                    if (p.norm) rx[i].load(x + (h0 + i * RPW) * R.xh, l);
+                    rg[i].load(g + (h0 + i * RPW) * R.gh, l);
+                }
+            l.angles(p, unit, token);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const bool on = l.in && h0 + i * RPW < R.heads;
+                float a[8] = {};
+                if (on) rg[i].unpack(a);
+                l.rotate(a, true);
+                if (p.norm) {
+                    float v[8] = {}, ss = 0.f, dot = 0.f;
+                    if (on) rx[i].unpack(v);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
+                    const float r = rsqrtf(row_sum<LPR>(ss) / float(p.dim) + p.eps);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        dw[c] = fmaf(a[c] * r, v[c], dw[c]);
+                        a[c] *= w[c];
+                        dot = fmaf(v[c], a[c], dot);
+                    }
+                    const float m = row_sum<LPR>(dot) / float(p.dim) * r * r;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) a[c] = r * (a[c] - m * v[c]);
+                }
+                if (on) {
+                    io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c0, a);
+                    io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c1, a + 4);
+                }
+            }
+        }
+        if (!R.w) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int m = LPR; m < 64; m <<= 1) dw[c] += __shfl_xor(dw[c], m);
+        __syncthreads(); // the other kind's shares have been read
+        if (sub == 0)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) part[wave][unit * 8 + c] = dw[c];
+        __syncthreads();
+        if (wave == 0 && sub == 0 && l.in) {
+            float *o = p.part + (int64_t(blockIdx.x) * 2 + kind) * p.dim;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                float s = 0.f;
+#pragma unroll
+                for (int v = 0; v < NW; ++v) s += part[v][unit * 8 + c];
+                o[c < 4 ? l.c0 + c : l.c1 + c - 4] = s;
+            }
+        }
+    }
+}
+
+// Sum of the workgroups' shares: 16 channels by 64 strips of workgroups.
+__global__ __launch_bounds__(1024) void k_norm_rotate_sum(const float *part, int n, int dim, float *dq, float *dk) {
+    __shared__ float s[64][17];
+    const int c = blockIdx.x * 16 + threadIdx.x % 16, strip = threadIdx.x / 16, kind = blockIdx.y;
+    float *out = kind ? dk : dq;
+    if (!out) return;
+    float a = 0.f;
+    if (c < dim)
+        for (int i = strip; i < n; i += 64) a += part[(int64_t(i) * 2 + kind) * dim + c];
+    s[strip][threadIdx.x % 16] = a;
+    __syncthreads();
+    for (int m = 32; m > 0; m >>= 1) {
+        if (strip < m) s[strip][threadIdx.x % 16] += s[strip + m][threadIdx.x % 16];
+        __syncthreads();
+    }
+    if (strip == 0 && c < dim) out[c] = s[0][threadIdx.x];
+}
+
+// Lanes of a row: the power of two that holds dim / 8.
+constexpr int rot_lanes(int dim) {
+    int n = 1;
+    while (n * 8 < dim) n *= 2;
+    return n;
+}
+
+template <typename IO, int LPR>
+hipError_t launch_rotary(const RotParams &p, int64_t grid, bool back, hipStream_t s) {
+    if (back) hipLaunchKernelGGL((k_norm_rotate_backward<IO, LPR>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
+    else hipLaunchKernelGGL((k_norm_rotate<IO, LPR>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t launch_rotary_io(const RotParams &p, int64_t grid, bool back, hipStream_t s) {
+    switch (rot_lanes(p.dim)) {
+    case 1: return launch_rotary<IO, 1>(p, grid, back, s);
+    case 2: return launch_rotary<IO, 2>(p, grid, back, s);
+    case 4: return launch_rotary<IO, 4>(p, grid, back, s);
+    case 8: return launch_rotary<IO, 8>(p, grid, back, s);
+    case 16: return launch_rotary<IO, 16>(p, grid, back, s);
+    case 32: return launch_rotary<IO, 32>(p, grid, back, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+} // namespace m3
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+m3_status_t check_shape(const m3_rotary_shape_t *s) {
+    if (!s) return M3_ERR_INVALID_ARGUMENT;
+    if (s->io_dtype != M3_DTYPE_F32 && s->io_dtype != M3_DTYPE_BF16) return M3_ERR_INVALID_ARGUMENT;
+    if (s->tokens < 0 || s->q_heads < 1 || s->k_heads < 0 || s->dim < 1 || s->rot < 1 || s->rot > s->dim || s->axes < 1)
+        return M3_ERR_INVALID_ARGUMENT;
+    if (s->norm && !(s->eps >= 0.f)) return M3_ERR_INVALID_ARGUMENT;
+    if (s->dim % 8 || s->dim > 256 || s->rot % 8 || s->axes > 4) return M3_ERR_UNSUPPORTED;
+    if (s->q_heads > (1 << 20) || s->k_heads > (1 << 20)) return M3_ERR_UNSUPPORTED;
+    if (double(s->tokens) * (double(s->q_heads) + s->k_heads + 2) > 2147483647.0) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+bool rows_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim, bool out) {
+    if (heads == 0) return true;
+    if (!r) return false;
+    if (tokens == 0) return true;
+    const int64_t t = r->token_stride, h = r->head_stride;
+    if (!r->data || !aligned16(r->data) || t < 0 || h < 0 || t >= (int64_t(1) << 24) || h >= (int64_t(1) << 40) || t % 8 || h % 8)
+        return false;
+    if (!out) return true;
+    const bool by_token = (tokens == 1 || t >= (heads - 1) * h + dim) && (heads == 1 || h >= dim);
+    const bool by_head = (heads == 1 || h >= (tokens - 1) * t + dim) && (tokens == 1 || t >= dim);
+    return by_token || by_head;
+}
+
+int32_t items(const m3_rotary_shape_t *s, int32_t heads) {
+    const int set = m3::kRows * (64 / m3::rot_lanes(s->dim));
+    return (heads + set - 1) / set;
+}
+
+// Workgroups of the gradients: four per compute unit at most, so that the
+// partial sums of the weights stay few.
+int64_t backward_grid(const m3_rotary_shape_t *s) {
+    const int64_t n = s->tokens * std::max(items(s, s->q_heads), items(s, s->k_heads));
+    return std::max<int64_t>(1, std::min<int64_t>((n + 3) / 4, 1024));
+}
+
+m3::RotParams params(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_rows_t *k, const void *pos,
+                     const float *freq, const float *qw, const float *kw, const m3_rows_t *qo, const m3_rows_t *ko) {
+    m3::RotParams p{};
+    const m3_rows_t *in[2] = {q, k}, *out[2] = {qo, ko};
+    const int32_t heads[2] = {s->q_heads, s->k_heads};
+    const float *w[2] = {qw, kw};
+    for (int i = 0; i < 2; ++i) {
+        if (heads[i] == 0) continue;
+        p.r[i].x = in[i]->data; p.r[i].xt = in[i]->token_stride; p.r[i].xh = in[i]->head_stride;
+        p.r[i].out = out[i]->data; p.r[i].ot = out[i]->token_stride; p.r[i].oh = out[i]->head_stride;
+        p.r[i].w = w[i];
+        p.r[i].heads = heads[i];
+        p.r[i].items = items(s, heads[i]);
+    }
+    p.tokens = s->tokens;
+    p.dim = s->dim;
+    p.rot = s->rot;
+    p.axes = s->axes;
+    p.pos64 = s->pos_int64;
+    p.halves = s->halves;
+    p.norm = s->norm;
+    p.eps = s->eps;
+    p.pos = pos;
+    p.freq = freq;
+    return p;
+}
+
+m3_status_t check_common(const m3_rotary_shape_t *s, const void *pos, const float *freq, const float *qw, const float *kw) {
+    if (s->tokens && (!pos || (reinterpret_cast<uintptr_t>(pos) & (s->pos_int64 ? 7 : 3)))) return M3_ERR_INVALID_ARGUMENT;
+    if (!freq || !aligned16(freq) || !aligned16(qw) || !aligned16(kw)) return M3_ERR_INVALID_ARGUMENT;
+    if ((qw || kw) && !s->norm) return M3_ERR_INVALID_ARGUMENT;
+    if (kw && s->k_heads == 0) return M3_ERR_INVALID_ARGUMENT;
+    return M3_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+m3_status_t m3_norm_rotate(const m3_rotary_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
+                           const void *positions, const float *inv_freq, const float *q_weight,
+                           const float *k_weight, const m3_rows_t *q_out, const m3_rows_t *k_out,
+                           hipStream_t stream) {
+    m3_status_t sc = check_shape(shape);
+    if (sc != M3_OK) return sc;
+    sc = check_common(shape, positions, inv_freq, q_weight, k_weight);
+    if (sc != M3_OK) return sc;
+    const int64_t T = shape->tokens;
+    if (!rows_ok(q, T, shape->q_heads, shape->dim, false) || !rows_ok(k, T, shape->k_heads, shape->dim, false) ||
+        !rows_ok(q_out, T, shape->q_heads, shape->dim, true) || !rows_ok(k_out, T, shape->k_heads, shape->dim, true))
+        return M3_ERR_INVALID_ARGUMENT;
+    if (T == 0) return M3_OK;
+    const m3::RotParams p = params(shape, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out);
+    const int64_t grid = (T * (p.r[0].items + p.r[1].items) + 3) / 4;
+    const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, grid, false, stream)
+                                                         : m3::launch_rotary_io<m3::bf16>(p, grid, false, stream);
+    return e == hipSuccess ? M3_OK : M3_ERR_HIP;
+}
+
+size_t m3_norm_rotate_backward_workspace_bytes(const m3_rotary_shape_t *shape) {
+    if (check_shape(shape) != M3_OK) return 0;
+    return size_t(backward_grid(shape)) * 2 * shape->dim * sizeof(float);
+}
+
+m3_status_t m3_norm_rotate_backward(const m3_rotary_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
+                                    const void *positions, const float *inv_freq, const float *q_weight,
+                                    const float *k_weight, const m3_rows_t *gq, const m3_rows_t *gk,
+                                    const m3_rows_t *dq, const m3_rows_t *dk, float *dq_weight, float *dk_weight,
+                                    void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    m3_status_t sc = check_shape(shape);
+    if (sc != M3_OK) return sc;
+    sc = check_common(shape, positions, inv_freq, q_weight, k_weight);
+    if (sc != M3_OK) return sc;
+    const int64_t T = shape->tokens;
+    if (!rows_ok(q, T, shape->q_heads, shape->dim, false) || !rows_ok(k, T, shape->k_heads, shape->dim, false) ||
+        !rows_ok(gq, T, shape->q_heads, shape->dim, false) || !rows_ok(gk, T, shape->k_heads, shape->dim, false) ||
+        !rows_ok(dq, T, shape->q_heads, shape->dim, true) || !rows_ok(dk, T, shape->k_heads, shape->dim, true))
+        return M3_ERR_INVALID_ARGUMENT;
+    if (!q_weight != !dq_weight || !k_weight != !dk_weight) return M3_ERR_INVALID_ARGUMENT;
+    if ((reinterpret_cast<uintptr_t>(dq_weight) & 3) || (reinterpret_cast<uintptr_t>(dk_weight) & 3)) return M3_ERR_INVALID_ARGUMENT;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < m3_norm_rotate_backward_workspace_bytes(shape))
+        return M3_ERR_WORKSPACE;
+    m3::RotParams p = params(shape, q, k, positions, inv_freq, q_weight, k_weight, dq, dk);
+    p.r[0].g = gq->data; p.r[0].gt = gq->token_stride; p.r[0].gh = gq->head_stride;
+    if (shape->k_heads) { p.r[1].g = gk->data; p.r[1].gt = gk->token_stride; p.r[1].gh = gk->head_stride; }
+    p.part = static_cast<float *>(workspace);
+    const int64_t grid = backward_grid(shape);
+    const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, grid, true, stream)
+                                                         : m3::launch_rotary_io<m3::bf16>(p, grid, true, stream);
+    if (e != hipSuccess) return M3_ERR_HIP;
+    if (dq_weight || dk_weight) {
+        hipLaunchKernelGGL(m3::k_norm_rotate_sum, dim3(unsigned((shape->dim + 15) / 16), 2), dim3(1024), 0, stream,
+                           p.part, int(grid), shape->dim, dq_weight, dk_weight);
+        if (hipGetLastError() != hipSuccess) return M3_ERR_HIP;
+    }
+    return M3_OK;
+}
+
+} // extern "C"

@@ -1,0 +1,115 @@
+"""torch-facing wrapper of the norm of queries and keys for each head with the
+position rotation in the same pass (include/m3_rotary.h).
+
+    n = w x / sqrt(mean(x^2) + eps),    y = R(angle) n,
+    angle_i = sum_a positions[a, token] inv_freq[a, i]
+
+q [T,Hq,D], k [T,Hk,D] (or [B,T,H,D]) in float32 or bfloat16, strided as in
+``linear``; positions [T] or [axes,T], int32 or int64; inv_freq [n] or
+[axes,n] float32, which turns the first 2 n channels: the pairs (2i, 2i+1), or
+(i, i+n) with halves=True.  ``axes_table`` lays out the frequencies of several
+axes (time, height, width).  D and 2 n are multiples of 8, D up to 256.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import capi
+from .linear import _device, _rows
+from .mixer import _IO, _ptr, _stream
+
+
+def axes_table(inv_freq: torch.Tensor, sections, interleaved: bool = False) -> torch.Tensor:
+    """[axes,n] frequencies: pair i turns by the position of its axis.
+
+    ``sections`` gives each axis its number of pairs (their sum is n): runs of
+    pairs in the axes' order, or, ``interleaved``, dealt out in turn until an
+    axis has all of its own.
+    """
+    n = inv_freq.numel()
+    if inv_freq.dim() != 1 or sum(sections) != n or any(s < 0 for s in sections):
+        raise ValueError(f"sections must add up to {n} pairs, got {tuple(sections)}")
+    if interleaved:
+        left, axis = list(sections), []
+        while len(axis) < n:
+            for a, s in enumerate(left):
+                if s > 0:
+                    axis.append(a)
+                    left[a] -= 1
+    else:
+        axis = [a for a, s in enumerate(sections) for _ in range(s)]
+    pick = torch.tensor(axis, device=inv_freq.device) == torch.arange(len(sections), device=inv_freq.device)[:, None]
+    return torch.where(pick, inv_freq, torch.zeros_like(inv_freq)).float().contiguous()
+
+
+def _weight(w, name, d, device):
+    if w is None:
+        return None
+    if w.device != device or tuple(w.shape) != (d,):
+        raise ValueError(f"{name} must be [{d}] on {device}, got {tuple(w.shape)} on {w.device}")
+    return _ptr(w, name, torch.float32)
+
+
+def _common(q, k, positions, inv_freq, norm, eps, halves):
+    dev, io = _device(q), q.dtype
+    if io not in _IO:
+        raise ValueError(f"q must be float32 or bfloat16, got {io}")
+    (rq, (b, T, hq, d)), (rk, sk) = _rows(q, "q", io, dev), _rows(k, "k", io, dev)
+    if sk[:2] != (b, T) or sk[3] != d:
+        raise ValueError(f"q and k must share tokens and channels: {tuple(q.shape)}, {tuple(k.shape)}")
+    axes = 1 if inv_freq.dim() == 1 else inv_freq.shape[0]
+    if inv_freq.dim() not in (1, 2) or inv_freq.device != dev:
+        raise ValueError(f"inv_freq must be [n] or [axes,n] on {dev}, got {tuple(inv_freq.shape)} on {inv_freq.device}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
+    if positions.device != dev or positions.numel() != axes * T or (axes > 1 and positions.shape[0] != axes):
+        raise ValueError(f"positions must be [{axes},{T}] on {dev}, got {tuple(positions.shape)} on {positions.device}")
+    shape = capi.m3_rotary_shape_t(T, hq, sk[2], d, 2 * inv_freq.shape[-1], axes, _IO[io],
+                                   int(positions.dtype == torch.int64), int(bool(halves)), int(bool(norm)), eps)
+    return dev, io, shape, rq, rk, _ptr(positions, "positions", None), _ptr(inv_freq, "inv_freq", torch.float32), d
+
+
+def norm_rotate(q, k, positions, inv_freq, *, norm=True, eps=1e-6, q_weight=None, k_weight=None, halves=False,
+                q_out=None, k_out=None):
+    """Returns (q', k'), shaped like q and k (new ones, or ``q_out`` and
+    ``k_out``, which may be q and k themselves).  ``q_weight`` and ``k_weight``
+    [D] float32 belong to the norm; norm=False only turns."""
+    dev, io, shape, rq, rk, pos, freq, d = _common(q, k, positions, inv_freq, norm, eps, halves)
+    q_out = torch.empty(q.shape, device=dev, dtype=io) if q_out is None else q_out
+    k_out = torch.empty(k.shape, device=dev, dtype=io) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must be shaped like q and k")
+    rc = capi.m3_norm_rotate(shape, rq, rk, pos, freq, _weight(q_weight, "q_weight", d, dev),
+                             _weight(k_weight, "k_weight", d, dev), _rows(q_out, "q_out", io, dev)[0],
+                             _rows(k_out, "k_out", io, dev)[0], _stream())
+    if rc != capi.M3_OK:
+        raise capi.M3Error(rc, "m3_norm_rotate")
+    return q_out, k_out
+
+
+def norm_rotate_backward(q, k, positions, inv_freq, gq, gk, *, norm=True, eps=1e-6, q_weight=None, k_weight=None,
+                         halves=False, workspace=None):
+    """Gradients of sum(gq * q') + sum(gk * k') for q', k' = norm_rotate(q, k,
+    ...): a dict of q and k, and q_weight and k_weight (float32) where given."""
+    dev, io, shape, rq, rk, pos, freq, d = _common(q, k, positions, inv_freq, norm, eps, halves)
+    if gq.shape != q.shape or gk.shape != k.shape:
+        raise ValueError("gq and gk must be shaped like q and k")
+    need = capi.m3_norm_rotate_backward_workspace_bytes(shape)
+    if need == 0:
+        raise capi.M3Error(capi.M3_ERR_UNSUPPORTED, "m3_norm_rotate_backward_workspace_bytes")
+    if workspace is None:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    g = {"q": torch.empty(q.shape, device=dev, dtype=io), "k": torch.empty(k.shape, device=dev, dtype=io)}
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            g[name] = torch.empty(d, device=dev, dtype=torch.float32)
+    rc = capi.m3_norm_rotate_backward(
+        shape, rq, rk, pos, freq, _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev),
+        _rows(gq, "gq", io, dev)[0], _rows(gk, "gk", io, dev)[0], _rows(g["q"], "dq", io, dev)[0],
+        _rows(g["k"], "dk", io, dev)[0], *(g[n].data_ptr() if n in g else None for n in ("q_weight", "k_weight")),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream())
+    if rc != capi.M3_OK:
+        raise capi.M3Error(rc, "m3_norm_rotate_backward")
+    return g

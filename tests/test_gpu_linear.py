@@ -1,0 +1,461 @@
+"""Linear attention with a decay for each head on the GPU against the fp64
+oracle (oracle/linear.py): prompt pass, gradients, single-token step.
+
+Tolerances.  Running the recurrence on absolute values gives, for every entry
+of a result, the sum A of the sizes of its terms.  With bf16 I/O a term meets
+two roundings of at most 2^-8 that do not both reach it (the weight q.k of its
+own chunk, or the entry of the chunk's starting state), and the result one
+more, so |error| <= 2^-8 (A + |o|) up to second order; as independent errors
+the two have a norm of at most 2^-8 sqrt(2/3) of the terms'.  fp32 results
+(states, and everything with fp32 I/O) add about Dk + Dv + 64 + the number of
+chunks terms in fp32, with decay factors of a few steps: at most 512 x 2^-24 A
+for these sizes.
+"""
+import numpy as np
+import pytest
+
+from oracle import linear as ol
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U16, U32 = 2.0 ** -8, 512 * 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _bound(A, out, dtype):
+    return U32 * A + (1.01 * U16 * (A + np.abs(out)) if dtype == torch.bfloat16 else 0) + 1e-30
+
+
+def _check(name, got, want, A, dtype):
+    got = _np(got)
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    assert np.isfinite(got).all(), f"{name}: not finite"
+    over = np.abs(got - want) / _bound(A, want, dtype)
+    worst = float(over.max()) if over.size else 0.0
+    n = np.linalg.norm(want)
+    rel = float(np.linalg.norm(got - want) / n) if n else 0.0
+    print(f"{name}: {worst:.3f} of the bound, relative {rel:.2e}", flush=True)
+    assert worst <= 1.0, name
+
+
+class Case:
+    """Inputs on the device and, rounded to their type, in fp64."""
+
+    def __init__(self, lengths, heads, dk, dv, io, seed=0, state=False, sd=torch.float32, decay=(0.002, 0.7), fused=False):
+        g = torch.Generator().manual_seed(seed)
+        T, H = sum(lengths), max(heads)
+        dt = DT[io]
+        if fused:
+            assert dk == dv
+            rows = torch.randn(T, sum(heads), dk, generator=g).to(dt).cuda()
+            self.q, self.k, self.v = rows.split(heads, dim=1)
+        else:
+            self.q, self.k, self.v = (torch.randn(T, h, d, generator=g).to(dt).cuda()
+                                      for h, d in zip(heads, (dk, dk, dv)))
+        self.go = torch.randn(T, H, dv, generator=g).to(dt).cuda()
+        self.ld = -torch.exp(torch.empty(H).uniform_(np.log(decay[0]), np.log(decay[1]), generator=g)).cuda()
+        self.cu = [0, *np.cumsum(lengths).tolist()]
+        self.cu_dev = torch.tensor(self.cu, dtype=torch.int32, device="cuda")
+        shape = (len(lengths), H, dk, dv)
+        self.state = torch.randn(shape, generator=g).to(sd).cuda() if state else None
+        self.gfinal = torch.randn(shape, generator=g).cuda() if state else None
+        self.dt, self.lengths = dt, lengths
+
+    def args(self):
+        return self.q, self.k, self.v, self.ld
+
+    def host(self, absolute=False):
+        f = (lambda t: np.abs(_np(t))) if absolute else _np
+        return [f(t) for t in (self.q, self.k, self.v)] + [_np(self.ld)]
+
+
+def _run_prefill(c, **kw):
+    from mamba_selective_ssm_ssd_amd import linear
+    final = torch.empty_like(c.state) if c.state is not None else None
+    o, final = linear.prefill(*c.args(), state=c.state, final=final, cu_seqlens=c.cu_dev, **kw)
+    torch.cuda.synchronize()
+    return o, final
+
+
+def _oracle_prefill(c):
+    s, sa = (None, None) if c.state is None else (_np(c.state), np.abs(_np(c.state)))
+    return ol.prefill(*c.host(), c.cu, s), ol.prefill(*c.host(True), c.cu, sa)
+
+
+def _check_prefill(c, **kw):
+    o, final = _run_prefill(c, **kw)
+    (wo, wf), (ao, af) = _oracle_prefill(c)
+    _check("o", o, wo, ao, c.dt)
+    _check("final", final, wf, af, final.dtype)
+
+
+HEADS = [(3, 3, 3), (4, 2, 1), (1, 1, 4), (2, 6, 3)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(8, 8), (16, 40), (32, 32), (64, 64), (64, 128), (128, 64), (96, 80), (128, 128), (32, 128), (128, 24)])
+def test_prefill_sizes(io, dk, dv):
+    _check_prefill(Case([70, 1, 0, 33], (2, 2, 2), dk, dv, io, seed=dk + dv, state=True))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200])
+def test_prefill_lengths(io, n):
+    _check_prefill(Case([n], (2, 1, 2), 64, 32, io, seed=n, state=n % 2 == 1), max_seqlen=n)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", HEADS)
+def test_prefill_head_groups(io, heads):
+    _check_prefill(Case([65, 40], heads, 64, 64, io, seed=7, state=True, fused=True))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[1500], [700, 0, 1, 900, 257], [256, 512, 1024], [5, 1300, 63]])
+@pytest.mark.parametrize("state", [False, True])
+def test_prefill_cut_sequences(io, lengths, state):
+    from mamba_selective_ssm_ssd_amd import capi, linear
+    c = Case(lengths, (2, 2, 2), 64, 64, io, seed=sum(lengths), state=state)
+    rc, seg, _ = capi.m3_linear_plan(linear.make_shape(len(lengths), sum(lengths), 2, 2, 2, 64, 64, c.dt))
+    assert rc == 0 and 0 < seg < max(lengths)
+    _check_prefill(c)
+
+
+@pytest.mark.parametrize("state", [False, True])
+def test_prefill_hint_changes_nothing_but_rounding(state):
+    """max_seqlen is only a hint: too small, too large or absent."""
+    c = Case([600, 900], (2, 2, 2), 64, 64, "bf16", seed=3, state=state)
+    for hint in (None, 1, 600, 900, 100000):
+        _check_prefill(c, max_seqlen=hint)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_decays_at_the_ends(io):
+    """No decay, a slow one over many chunks, a fast one, and one that forgets everything."""
+    c = Case([1100], (5, 5, 5), 32, 32, io, seed=4, state=True)
+    c.ld[:] = torch.tensor([0.0, -1e-6, -1e-3, -20.0, -float("inf")])
+    _check_prefill(c)
+    _check_backward(c)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_dense_and_bf16_states(io):
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([90, 90, 90], (4, 2, 4), 64, 64, io, seed=5, state=True, sd=torch.bfloat16)
+    dense = [t.view(3, 90, *t.shape[1:]) for t in (c.q, c.k, c.v)]
+    final = torch.empty_like(c.state)
+    o, _ = linear.prefill(*dense, c.ld, state=c.state, final=final)
+    assert o.shape == (3, 90, 4, 64) and final.dtype == torch.bfloat16
+    (wo, wf), (ao, af) = _oracle_prefill(c)
+    _check("o", o.flatten(0, 1), wo, ao, c.dt)
+    # the bf16 state is one rounding of the fp32 one
+    assert (np.abs(_np(final) - wf) <= 1.01 * U16 * np.abs(wf) + U32 * af).all()
+
+
+def test_prefill_in_place_state_and_slots():
+    from mamba_selective_ssm_ssd_amd import linear
+    for lengths in ([40, 0, 70, 1], [700, 0, 900, 1]):
+        c = Case(lengths, (2, 2, 2), 64, 64, "bf16", seed=6, state=True)
+        pool = torch.randn(9, 2, 64, 64, device="cuda")
+        slots = torch.tensor([7, 0, 3, 5], dtype=torch.int32, device="cuda")
+        pool[slots.long()] = c.state
+        before = pool.clone()
+        o, out = linear.prefill(*c.args(), state=pool, cu_seqlens=c.cu_dev, slots=slots)
+        assert out is pool
+        (wo, wf), (ao, af) = _oracle_prefill(c)
+        _check("o", o, wo, ao, c.dt)
+        _check("final", pool[slots.long()], wf, af, torch.float32)
+        rest = [1, 2, 4, 6, 8]
+        assert torch.equal(pool[rest], before[rest])
+
+
+def test_prefill_padding_slots_tail_rows_and_repeated_slots():
+    from mamba_selective_ssm_ssd_amd import linear
+    for lengths in ([40, 30, 70, 20], [400, 300, 700, 600]):
+        c = Case(lengths, (2, 2, 2), 64, 64, "bf16", seed=8, state=True)
+        T = sum(lengths)
+        q, k, v = (torch.cat([t, torch.full_like(t[:5], float("nan"))]) for t in (c.q, c.k, c.v))
+        pool = torch.randn(6, 2, 64, 64, device="cuda")
+        slots = torch.tensor([4, -1, 4, 99], dtype=torch.int32, device="cuda")
+        pool[4] = c.state[0]
+        before = pool.clone()
+        o = torch.full((T + 5, 2, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+        linear.prefill(q, k, v, c.ld, state=pool, cu_seqlens=c.cu_dev, slots=slots, o=o)
+        (wo, wf), (ao, af) = _oracle_prefill(c)
+        a, b, d = c.cu[1], c.cu[2], c.cu[3]
+        _check("o", o[:a], wo[:a], ao[:a], c.dt)
+        assert (o[a:b] == 7).all() and torch.isnan(o[b:d].float()).all() and (o[d:] == 7).all()
+        _check("state", pool[4], wf[0], af[0], torch.float32)
+        rest = [0, 1, 2, 3, 5]
+        assert torch.equal(pool[rest], before[rest])
+
+
+def _run_backward(c, **kw):
+    from mamba_selective_ssm_ssd_amd import linear
+    g = linear.backward(*c.args(), c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev, **kw)
+    torch.cuda.synchronize()
+    return g
+
+
+def _check_backward(c, **kw):
+    g = _run_backward(c, **kw)
+    pick = (lambda f: [None if t is None else f(_np(t)) for t in (c.state, c.gfinal)])
+    want = ol.backward(*c.host(), _np(c.go), c.cu, *pick(lambda x: x))
+    size = ol.backward(*c.host(True), np.abs(_np(c.go)), c.cu, *pick(np.abs))
+    for i, n in enumerate("qkv"):
+        assert g[n].dtype == c.dt
+        _check("d" + n, g[n], want[i], size[i], c.dt)
+    if c.state is not None:
+        _check("dstate", g["state"], want[3], size[3], torch.float32)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(8, 16), (32, 32), (64, 64), (64, 128), (128, 64), (96, 80), (128, 128), (24, 128)])
+def test_backward_sizes(io, dk, dv):
+    _check_backward(Case([70, 1, 0, 33], (2, 2, 2), dk, dv, io, seed=dk + dv, state=True))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", HEADS)
+def test_backward_head_groups(io, heads):
+    _check_backward(Case([65, 40], heads, 64, 64, io, seed=9, state=heads[0] != 3, fused=True))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[1500], [700, 0, 1, 900, 257]])
+@pytest.mark.parametrize("state", [False, True])
+def test_backward_cut_sequences(io, lengths, state):
+    from mamba_selective_ssm_ssd_amd import capi, linear
+    c = Case(lengths, (2, 2, 2), 64, 64, io, seed=10, state=state)
+    rc, _, seg = capi.m3_linear_plan(linear.make_shape(len(lengths), sum(lengths), 2, 2, 2, 64, 64, c.dt))
+    assert rc == 0 and 0 < seg < max(lengths)
+    _check_backward(c)
+
+
+@pytest.mark.parametrize("heads", [(2, 2, 2), (2, 1, 1)])
+def test_backward_rows_outside_every_sequence_are_zero(heads):
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([30, 40], heads, 64, 64, "bf16", seed=11)
+    pad = lambda t: torch.cat([t[:3], t, t[:9]])  # noqa: E731
+    cu = c.cu_dev + 3
+    g = linear.backward(pad(c.q), pad(c.k), pad(c.v), c.ld, pad(c.go), cu_seqlens=cu)
+    ref = linear.backward(*c.args(), c.go, cu_seqlens=c.cu_dev)
+    for n in "qkv":
+        assert torch.equal(g[n][3:73], ref[n]) and not g[n][:3].any() and not g[n][73:].any()
+
+
+def test_backward_matches_differences_of_the_kernel_itself():
+    """A directional difference of the fp32 prompt pass."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([50, 300], (2, 1, 2), 32, 48, "f32", seed=12, state=True, decay=(0.05, 0.7))
+
+    def loss(q, k, v, s):
+        o, f = linear.prefill(q, k, v, c.ld, state=s, final=torch.empty_like(s), cu_seqlens=c.cu_dev)
+        return float((o.double() * c.go.double()).sum() + (f.double() * c.gfinal.double()).sum())
+
+    g = _run_backward(c)
+    x = [c.q, c.k, c.v, c.state]
+    for i, n in enumerate(("q", "k", "v", "state")):
+        d = torch.randn(x[i].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(i))
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + 0.25 * d, x[i] - 0.25 * d
+        # o is linear in each operand: the difference is exact but for fp32 rounding
+        diff, want = (loss(*up) - loss(*down)) / 0.5, float((g[n].double() * d.double()).sum())
+        assert abs(diff - want) <= 1e-4 * float((g[n].double() * d.double()).abs().sum()), (n, diff, want)
+
+
+def _oracle_step(c, pool, slots):
+    q, k, v, ld = c.host()
+    cu = list(range(len(slots) + 1))
+    ok = [ol.prefill(*x, cu, s) for x, s in (((q, k, v, ld), pool[slots]), ((*(abs(t) for t in (q, k, v)), ld), abs(pool[slots])))]
+    return ok
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("sd", ["f32", "bf16"])
+@pytest.mark.parametrize("B,heads,dk,dv", [(1, (1, 1, 1), 8, 8), (3, (4, 2, 1), 64, 64), (5, (2, 2, 2), 128, 128), (2, (3, 3, 3), 96, 80),
+                                           (70, (2, 4, 16), 32, 72), (130, (8, 8, 8), 64, 128), (300, (4, 1, 4), 16, 8)])
+def test_decode_step(io, sd, B, heads, dk, dv):
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([1] * B, heads, dk, dv, io, seed=B, fused=dk == dv)
+    H = max(heads)
+    pool = torch.randn(B + 3, H, dk, dv, generator=torch.Generator().manual_seed(B)).to(DT[sd]).cuda()
+    slots = torch.randperm(B + 3, generator=torch.Generator().manual_seed(1))[:B]
+    before = pool.clone()
+    o = linear.decode_step(*c.args(), pool, slots=slots.int().cuda())
+    (wo, wf), (ao, af) = _oracle_step(c, _np(before), slots.numpy())
+    # fp32 arithmetic throughout: only the result is rounded
+    assert (np.abs(_np(o) - wo) <= U32 * ao + (1.01 * U16 * np.abs(wo) if io == "bf16" else 0)).all()
+    assert (np.abs(_np(pool[slots.cuda()]) - wf) <= U32 * af + (1.01 * U16 * np.abs(wf) if sd == "bf16" else 0)).all()
+    rest = [i for i in range(B + 3) if i not in set(slots.tolist())]
+    assert torch.equal(pool[rest], before[rest])
+    # without slots: the first B states
+    pool = before.clone()
+    o2 = linear.decode_step(*c.args(), pool[:B])
+    (wo, wf), (ao, af) = _oracle_step(c, _np(before), np.arange(B))
+    assert (np.abs(_np(o2) - wo) <= U32 * ao + (1.01 * U16 * np.abs(wo) if io == "bf16" else 0)).all()
+    assert torch.equal(pool[B:], before[B:])
+
+
+def test_decode_step_padding_and_repeated_slots():
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([1] * 6, (2, 2, 2), 64, 64, "bf16", seed=20)
+    pool = torch.randn(4, 2, 64, 64, device="cuda")
+    before = pool.clone()
+    slots = torch.tensor([2, -1, 2, 0, 4, 0], dtype=torch.int32, device="cuda")
+    o = torch.full((6, 2, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    linear.decode_step(*c.args(), pool, slots=slots, o=o)
+    ref = before.clone()
+    o_ref = linear.decode_step(*(t[[0, 3]] for t in c.args()[:3]), c.ld, ref, slots=slots[[0, 3]].contiguous())
+    assert torch.equal(pool, ref) and torch.equal(o[[0, 3]], o_ref)
+    assert (o[[1, 4]] == 7).all() and torch.isnan(o[[2, 5]].float()).all()
+
+
+def test_slow_decay_over_many_steps():
+    """4000 steps of a decay so slow that rounding it to 24 bits would show."""
+    from mamba_selective_ssm_ssd_amd import linear
+    ld = torch.tensor([-1e-5], device="cuda")
+    pool = torch.ones(1, 1, 32, 32, device="cuda")
+    z = torch.zeros(1, 1, 32, device="cuda")
+    for _ in range(4000):
+        linear.decode_step(z, z, z, ld, pool)
+    want = float(np.exp(float(ld[0]) * 4000.0))
+    # one fma of half a step per token: 4000 x 2^-25 as a walk, 4 sigma
+    assert abs(float(pool.double().mean()) - want) <= 4 * np.sqrt(4000.0) * 2.0 ** -25
+    ones = torch.ones(1, 1, 32, 32, device="cuda")
+    zz = torch.zeros(60000, 1, 32, device="cuda")
+    _, f = linear.prefill(zz, zz, zz, ld, state=ones, final=torch.empty_like(ones))
+    want = float(np.exp(float(ld[0]) * 60000.0))
+    assert abs(float(f.double().mean()) - want) <= 4 * np.sqrt(2000.0) * 2.0 ** -24
+
+
+def test_prompt_then_steps_is_the_longer_prompt():
+    """The operators together, as a layer uses them: rows normed and turned,
+    the prompt, then token by token."""
+    from mamba_selective_ssm_ssd_amd import linear, rotary
+    T, n, H, D = 150, 130, 4, 64
+    g = torch.Generator().manual_seed(30)
+    qkv = torch.randn(T, 3 * H, D, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = qkv.split(H, dim=1)
+    ld = -torch.tensor([0.5, 0.1, 0.02, 0.004], device="cuda")
+    freq = 10000.0 ** (-torch.arange(32, device="cuda") / 32.0)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    qr, kr = rotary.norm_rotate(q, k, pos, freq)
+    whole, end = linear.prefill(qr, kr, v, ld)
+    qp, kp = rotary.norm_rotate(q[:n], k[:n], pos[:n], freq)
+    o, state = linear.prefill(qp, kp, v[:n], ld)
+    rows = [o]
+    for t in range(n, T):
+        qs, ks = rotary.norm_rotate(q[t:t + 1], k[t:t + 1], pos[t:t + 1], freq)
+        rows.append(linear.decode_step(qs, ks, v[t:t + 1], ld, state))
+    wo, wf = ol.prefill(_np(qr), _np(kr), _np(v), _np(ld), [0, T])
+    ao, af = ol.prefill(*(np.abs(_np(t)) for t in (qr, kr, v)), _np(ld), [0, T])
+    _check("prompt", whole, wo, ao, torch.bfloat16)
+    _check("pieces", torch.cat(rows), wo, ao, torch.bfloat16)
+    _check("end", end, wf, af, torch.float32)
+    _check("state", state, wf, af, torch.float32)
+
+
+def test_non_finite_tokens_stay_in_sequence_head_and_behind_their_chunk():
+    c = Case([200, 700], (3, 3, 3), 64, 64, "bf16", seed=13)
+    o0, f0 = _run_prefill(c)
+    for bad in (float("nan"), float("inf")):
+        for t in (70, 200 + 333):
+            v = c.v.clone()
+            c.v = v.clone()
+            c.v[t, 1, 5] = bad
+            o1, f1 = _run_prefill(c)
+            c.v = v
+            b = int(t >= 200)
+            lo = c.cu[b] + (t - c.cu[b]) // 64 * 64
+            same = torch.ones_like(o0, dtype=torch.bool)
+            same[lo:c.cu[b + 1], 1, 5] = False
+            assert torch.equal(o0[same], o1[same])
+            assert not torch.isfinite(o1[t:c.cu[b + 1], 1, 5].float()).any()
+            same = torch.ones_like(f0, dtype=torch.bool)
+            same[b, 1, :, 5] = False
+            assert torch.equal(f0[same], f1[same])
+
+
+def test_results_do_not_depend_on_the_run_or_the_neighbours():
+    """Bit for bit: twice the same call, on another stream, with garbage in the workspace."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([700, 90, 300], (4, 2, 2), 64, 64, "bf16", seed=14, state=True)
+    o0, f0 = _run_prefill(c)
+    g0 = _run_backward(c)
+    ws = torch.full((linear.workspace_bytes(c.q, c.k, c.v, c.cu_dev),), 255, dtype=torch.uint8, device="cuda")
+    wb = torch.full((linear.workspace_bytes(c.q, c.k, c.v, c.cu_dev, backward=True),), 255, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o1, f1 = _run_prefill(c, workspace=ws)
+        g1 = _run_backward(c, workspace=wb)
+    assert torch.equal(o0, o1) and torch.equal(f0, f1) and all(torch.equal(g0[n], g1[n]) for n in g0)
+
+
+def test_graph_capture_and_replay():
+    from mamba_selective_ssm_ssd_amd import linear, rotary
+    c = Case([600, 0, 300], (4, 2, 2), 64, 64, "bf16", seed=15, state=True)
+    d = Case([1, 1, 1], (4, 2, 2), 64, 64, "bf16", seed=16)
+    freq = 10000.0 ** (-torch.arange(32, device="cuda") / 32.0)
+    pos = torch.arange(900, device="cuda", dtype=torch.int32)
+    w = torch.linspace(0.5, 1.5, 64, device="cuda")
+    final, pool = torch.empty_like(c.state), c.state.clone()
+
+    def work():
+        q, k = rotary.norm_rotate(c.q, c.k, pos, freq, q_weight=w, k_weight=w)
+        o, _ = linear.prefill(q, k, c.v, c.ld, state=c.state, final=final, cu_seqlens=c.cu_dev)
+        g = linear.backward(q, k, c.v, c.ld, c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev)
+        r = rotary.norm_rotate_backward(c.q, c.k, pos, freq, g["q"], g["k"], q_weight=w, k_weight=w)
+        s = linear.decode_step(*d.args(), pool)
+        return [o, final, s, *g.values(), *r.values()]
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for i in range(3):
+        c.q.normal_(generator=torch.Generator("cuda").manual_seed(i))
+        pool.copy_(c.state)
+        want = [t.clone() for t in work()]
+        pool.copy_(c.state)
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def test_device_refusals():
+    from mamba_selective_ssm_ssd_amd import capi, linear
+    c = Case([10], (2, 2, 2), 64, 64, "bf16", seed=17)
+    with pytest.raises(capi.M3Error):                                   # rows that are not 16-byte aligned
+        linear.prefill(torch.randn(10, 2, 65, device="cuda").bfloat16()[..., 1:], c.k, c.v, c.ld)
+    with pytest.raises(ValueError):                                     # channels with a stride
+        linear.prefill(torch.randn(10, 2, 128, device="cuda").bfloat16()[..., ::2], c.k, c.v, c.ld)
+    with pytest.raises(capi.M3Error):                                   # a head count that does not divide
+        linear.prefill(c.q, c.k, torch.randn(10, 3, 64, device="cuda").bfloat16(),
+                       torch.zeros(3, device="cuda"))
+    with pytest.raises(capi.M3Error):                                   # a size outside the set
+        linear.prefill(torch.randn(10, 2, 136, device="cuda").bfloat16(), torch.randn(10, 2, 136, device="cuda").bfloat16(), c.v, c.ld)
+    with pytest.raises(capi.M3Error):
+        linear.prefill(*c.args(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    for kw in (dict(o=torch.empty(9, 2, 64, device="cuda", dtype=torch.bfloat16)), dict(state=torch.zeros(2, 2, 64, 64, device="cuda")),
+               dict(cu_seqlens=torch.tensor([0, 10], device="cuda")), dict(cu_seqlens=torch.tensor([0, 10], dtype=torch.int32)),
+               dict(slots=torch.zeros(1, dtype=torch.int32, device="cuda")), dict(state=torch.zeros(1, 2, 64, 64, device="cuda", dtype=torch.float16))):
+        with pytest.raises(ValueError):
+            linear.prefill(*c.args(), **kw)
+    with pytest.raises(ValueError):
+        linear.prefill(c.q.cpu(), c.k, c.v, c.ld)
+    with pytest.raises(ValueError):
+        linear.prefill(c.q, c.k.float(), c.v, c.ld)
+    with pytest.raises(ValueError):
+        linear.backward(*c.args(), c.go[:5])
+    with pytest.raises(capi.M3Error):                                   # outputs that overlap themselves
+        linear.prefill(*c.args(), o=torch.empty(1, 2, 64, device="cuda", dtype=torch.bfloat16).expand(10, 2, 64))
