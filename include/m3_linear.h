@@ -17,7 +17,9 @@
  * channels of one row contiguous; an m3_rows_t names the strides of the other
  * two axes in elements, so views of one projection's rows are taken as they
  * are.  Rows must be 16-byte aligned: the base pointer, and both strides
- * multiples of 8 elements.  Strides are non-negative and below 2^24.
+ * multiples of 8 elements.  The tokens' stride is at least the row's channels
+ * and below 2^24 (of no account with one token), the heads' from 0 to below
+ * 2^40.
  *
  * Sequences.  cu_seqlens (device, int32, batch + 1 entries, ascending from 0
  * to at most `tokens`) gives sequence b the tokens cu_seqlens[b] up to

@@ -309,19 +309,19 @@ def m3_linear_plan(shape: m3_linear_shape_t):
 
 
 def m3_linear_prefill(*args) -> int:
-    return load().m3_linear_prefill(*args)
+    return (_lib or load()).m3_linear_prefill(*args)
 
 
 def m3_linear_decode_step(*args) -> int:
-    return load().m3_linear_decode_step(*args)
+    return (_lib or load()).m3_linear_decode_step(*args)
 
 
 def m3_linear_prefill_backward(*args) -> int:
-    return load().m3_linear_prefill_backward(*args)
+    return (_lib or load()).m3_linear_prefill_backward(*args)
 
 
 def m3_norm_rotate(*args) -> int:
-    return load().m3_norm_rotate(*args)
+    return (_lib or load()).m3_norm_rotate(*args)
 
 
 def m3_norm_rotate_backward_workspace_bytes(shape: m3_rotary_shape_t) -> int:
@@ -329,4 +329,4 @@ def m3_norm_rotate_backward_workspace_bytes(shape: m3_rotary_shape_t) -> int:
 
 
 def m3_norm_rotate_backward(*args) -> int:
-    return load().m3_norm_rotate_backward(*args)
+    return (_lib or load()).m3_norm_rotate_backward(*args)

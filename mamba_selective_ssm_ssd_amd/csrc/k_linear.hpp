@@ -44,18 +44,19 @@ struct LinParams {
     LinRole role[3];
     int32_t nroles, H, ztiles;
     int32_t tail;            // extra workgroups per scan that zero the rows outside every sequence
-    int64_t batch, tokens, nwork; // nwork: workgroups without the tail
+    int32_t nwork;           // workgroups without the tail
+    int64_t batch, tokens, each; // each: tokens of a sequence without cu
     const int32_t *cu;       // null: equal sequences
     const int32_t *slots;    // null: sequence b has state b
     int64_t nstates;
     const float *log_decay;
-    int64_t seglen;          // tokens per segment, 0: sequences are not cut
+    int32_t segbits;         // log2 of the tokens per segment, 0: sequences are not cut
     int64_t nseg;            // segment slots (batch when not cut)
 };
 
 // First token of sequence b, clamped to the rows there are.
 __device__ __forceinline__ int64_t lin_start(const LinParams &p, int64_t b) {
-    if (!p.cu) return b * (p.tokens / p.batch);
+    if (!p.cu) return b * p.each;
     const int64_t c = p.cu[b];
     return c < 0 ? 0 : c > p.tokens ? p.tokens : c;
 }
@@ -79,7 +80,7 @@ __device__ __forceinline__ int64_t lin_slot(const int32_t *slots, int64_t nstate
 // floor((start + n) / L) - floor(start / L) + 1 >= ceil(n / L), so the slots
 // of two sequences never meet, there are at most tokens / L + batch of them,
 // and the sequence of a slot is found by bisection without any table.
-__device__ __forceinline__ int64_t lin_first_slot(const LinParams &p, int64_t b) { return lin_start(p, b) / p.seglen + b; }
+__device__ __forceinline__ int64_t lin_first_slot(const LinParams &p, int64_t b) { return (lin_start(p, b) >> p.segbits) + b; }
 
 // ---------------------------------------------------------------------------
 // Operands as PL planes of bf16 whose sum is the value: one plane for bf16
@@ -102,6 +103,23 @@ __device__ __forceinline__ floatx4 lmma(floatx4 acc, const lfrag<PA> &a, const l
         for (int i = PA - 1; i >= 0; --i)
             if (s - i >= 0 && s - i < PB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[s - i], acc, 0, 0, 0);
     return acc;
+}
+
+// f(i, j) for the pairs of planes of a product, in that order.
+template <int PA, int PB, typename F>
+__device__ __forceinline__ void lpairs(F &&f) {
+    auto pair = [&](auto i, auto j) {
+        if constexpr (i.value < PA && j.value < PB) f(i, j);
+    };
+    typedef std::integral_constant<int, 0> c0;
+    typedef std::integral_constant<int, 1> c1;
+    typedef std::integral_constant<int, 2> c2;
+    pair(c2(), c0());
+    pair(c1(), c1());
+    pair(c0(), c2());
+    pair(c1(), c0());
+    pair(c0(), c1());
+    pair(c0(), c0());
 }
 
 template <int PL>
@@ -129,35 +147,37 @@ __device__ __forceinline__ lfrag<PL> lsplit(const float a[8]) {
 template <int PL>
 __device__ __forceinline__ void lunsplit(const lfrag<PL> &f, float a[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = 0.f;
-#pragma unroll
     for (int k = PL - 1; k >= 0; --k) {
         const uint4 w = __builtin_bit_cast(uint4, f.v[k]);
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            a[2 * i] += __uint_as_float(ws[i] << 16);
-            a[2 * i + 1] += __uint_as_float(ws[i] & 0xffff0000u);
+            const float lo = __uint_as_float(ws[i] << 16), hi = __uint_as_float(ws[i] & 0xffff0000u);
+            a[2 * i] = k + 1 < PL ? a[2 * i] + lo : lo;
+            a[2 * i + 1] = k + 1 < PL ? a[2 * i + 1] + hi : hi;
         }
     }
 }
 
 // ---------------------------------------------------------------------------
 // Tile of one scan.  Q rows per chunk, DX x DZ state columns of a workgroup of
-// four waves; z columns beyond DZ are another workgroup's.
+// four or eight waves; z columns beyond DZ are another workgroup's.
 // ---------------------------------------------------------------------------
-constexpr int kLT = 256; // threads
-
 template <typename IO, int DX, int DZ, bool OUT>
 struct LinCfg {
     static constexpr bool F32 = std::is_same<IO, float>::value;
     static constexpr int PL = F32 ? 3 : 1;
-    static constexpr int Q = F32 ? 32 : 64;
-    static constexpr int MP = DX / 32, NP = DZ / 32; // 32 x 32 blocks of the state
-    // the state's blocks over the four waves: MW along x, the rest along z
-    static constexpr int MW = MP < 4 ? MP : 4, NW = 4 / MW, NPW = (NP + NW - 1) / NW;
-    // the output's 16-row tiles over the waves: RW along the rows, the rest along z
-    static constexpr int RW = Q / 16, OW = 4 / RW, NPO = (NP + OW - 1) / OW;
+    static constexpr int Q = F32 || (OUT && DX == 128 && DZ == 128) ? 32 : 64;
+    static constexpr int MP = DX / 32, NP = DZ / 32; // 32 x 32 blocks of the state, 16 x 16 tiles in pairs
+    // the state's tiles over the waves: MW along x (MTW tiles each, a pair of
+    // one block where it is two), NW along z
+    static constexpr int W = !F32 && !OUT && DX == 128 && DZ == 128 ? 8 : 4, T = 64 * W;
+    static constexpr int MW = 2 * MP < W ? 2 * MP : W, MTW = 2 * MP / MW, NW = W / MW, NTW = 2 * NP / NW;
+    static_assert(MTW <= 2 && NTW >= 1, "tiles of a wave");
+    // the output's 16-row tiles over the waves: RW along the rows, OW along z (NOT tiles each)
+    static constexpr int RW = Q / 16, OW = W / RW, NOT = 2 * NP / OW;
+    static_assert(NOT >= 1 && (F32 || NOT % 2 == 0), "output tiles of a wave, pairs where two share a store");
+    static_assert(NW == 1 || OW == 1 || MW == RW, "a wave's tiles of the state and of the output start alike");
     static constexpr int KS = Q / 32; // 32-row steps of a product over the chunk's rows
     // LDS, in bf16 elements: x, y, z planes and the state's fragments
     static constexpr int XP = Q * DX, ZP = Q * DZ, SP = DX * DZ;
@@ -165,25 +185,21 @@ struct LinCfg {
     static constexpr size_t bytes = 2 * size_t(SO + (OUT ? PL * SP : 0));
 };
 
-// 16-byte units of a staged row are permuted by the row, so that 16 rows at
-// one unit (row reads) and four rows at four neighbouring units (transposing
-// reads) both touch every bank once.
+// A staged row's 16-byte units are permuted by the row, in pairs and within a
+// pair, so that 16 rows at one unit (row reads), and eight rows at one pair (the
+// transposing reads of 16 neighbouring columns), touch every bank once.
 template <int D>
 __device__ __forceinline__ int lin_at(int row, int unit) {
-    constexpr int U = D / 8;
-    const int f = ((row & 3) << 2 | (row >> 2 & 3));
-    const int h = U >= 16 ? f : U == 8 ? (((f >> 3) << 2) | (f & 3)) : (f & 3);
-    return row * D + ((unit ^ h) << 3);
+    constexpr int P = D / 16, SH = P >= 8 ? 0 : P == 4 ? 1 : 2;
+    return row * D + (((((unit >> 1) ^ (row >> SH & (P - 1))) << 1) | ((unit & 1) ^ (row >> 3 & 1))) << 3);
 }
 
-// Eight k-slots of one column of a staged matrix: rows 16 t0 + 4 g + v, then
-// 16 (t0 + 1) + 4 g + v.  Lane r of a group gets column
-// 32 blk + 8 (r / 4) + r % 4 + 4 half.
+// Eight k-slots of a column of a staged matrix: rows 16 t0 + 4 g + v, then
+// 16 (t0 + 1) + 4 g + v, read transposed: lane j of a group addresses four
+// columns of row j / 4, and gets column `j` of the group's 16.
 template <int PL, int D, int PS>
-__device__ __forceinline__ lfrag<PL> lin_col(const uint16_t *m, int t0, int blk, int half, int r16, int g) {
-    const int row = 16 * t0 + 4 * g + (r16 >> 2), unit = 4 * blk + (r16 & 3);
-    const uint16_t *p0 = m + lin_at<D>(row, unit) + 4 * half;
-    const uint16_t *p1 = m + lin_at<D>(row + 16, unit) + 4 * half;
+__device__ __forceinline__ lfrag<PL> lin_tr(const uint16_t *m, int row, int unit, int part) {
+    const uint16_t *p0 = m + lin_at<D>(row, unit) + 4 * part, *p1 = m + lin_at<D>(row + 16, unit) + 4 * part;
     lfrag<PL> f;
 #pragma unroll
     for (int k = 0; k < PL; ++k) {
@@ -191,6 +207,18 @@ __device__ __forceinline__ lfrag<PL> lin_col(const uint16_t *m, int t0, int blk,
         f.v[k] = bf16x8_from_words(a.x, a.y, b.x, b.y);
     }
     return f;
+}
+// Tile n of z: lane r has column 16 n + r.
+template <int PL, int D, int PS>
+__device__ __forceinline__ lfrag<PL> lin_zcol(const uint16_t *m, int t0, int n, int r16, int g) {
+    return lin_tr<PL, D, PS>(m, 16 * t0 + 4 * g + (r16 >> 2), 2 * n + (r16 >> 1 & 1), r16 & 1);
+}
+// Tile t of y: lane r has column 32 (t / 2) + 8 (r / 4) + r % 4 + 4 (t % 2), so
+// that the state's rows of two tiles are eight neighbours in one lane: the
+// k-slots of a row of x.
+template <int PL, int D, int PS>
+__device__ __forceinline__ lfrag<PL> lin_ycol(const uint16_t *m, int t0, int t, int r16, int g) {
+    return lin_tr<PL, D, PS>(m, 16 * t0 + 4 * g + (r16 >> 2), 4 * (t >> 1) + (r16 & 3), t & 1);
 }
 template <int PL, int D, int PS>
 __device__ __forceinline__ lfrag<PL> lin_row(const uint16_t *m, int row, int unit) {
@@ -201,22 +229,48 @@ __device__ __forceinline__ lfrag<PL> lin_row(const uint16_t *m, int row, int uni
     return f;
 }
 
+// Bounded access to the rows of one chunk.  A chunk of fewer than Q rows lies at
+// the end of its tile, so that what a row weighs at the chunk's end, and in the
+// rows behind it, is the same in every chunk; the rows before it read as zero
+// and are not written.  Offsets count from the chunk's lowest token: walking
+// forwards a row before the chunk lies below zero, which as an unsigned number
+// is beyond the end, walking backwards beyond the end itself.
+constexpr uint32_t kNowhere = 0xffffffe0u; // beyond the end of every buffer, with the 16 bytes behind it
+
+struct LinBuf {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ LinBuf(const void *base, uint32_t bytes)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00027000)) {}
+    __device__ __forceinline__ uint4 load(uint32_t at) const {
+        const u32x4_v v = __builtin_bit_cast(u32x4_v, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
+    // past: written past the caches (non-temporal)
+    __device__ __forceinline__ void store(uint32_t at, uint4 v, bool past) const {
+        const u32x4_v q{v.x, v.y, v.z, v.w};
+        if (past) __builtin_amdgcn_raw_buffer_store_b128(q, r, at, 0, 2);
+        else __builtin_amdgcn_raw_buffer_store_b128(q, r, at, 0, 0);
+    }
+    __device__ __forceinline__ float get(uint32_t at) const { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0)); }
+    __device__ __forceinline__ float get16(uint32_t at) const { return bits_to_f32(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0))); }
+    __device__ __forceinline__ void put(uint32_t at, float v) const { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at, 0, 0); }
+    __device__ __forceinline__ void put16(uint32_t at, float v) const { __builtin_amdgcn_raw_buffer_store_b16(f32_to_bits(v), r, at, 0, 0); }
+};
+
 // Eight consecutive elements as loaded.
 template <typename IO>
 struct lraw;
 template <>
 struct lraw<bf16> {
     uint4 a;
-    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const bf16 *p) { a = ld16(p); }
+    __device__ __forceinline__ void load(const LinBuf &r, uint32_t at) { a = r.load(at); }
     template <int PS>
     __device__ __forceinline__ void stage(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = a; }
 };
 template <>
 struct lraw<float> {
     uint4 a, b;
-    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const float *p) { a = ld16(p); b = ld16(p + 4); }
+    __device__ __forceinline__ void load(const LinBuf &r, uint32_t at) { a = r.load(at); b = r.load(at + 16); }
     template <int PS>
     __device__ __forceinline__ void stage(uint16_t *p) const {
         const float v[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
@@ -228,25 +282,37 @@ struct lraw<float> {
 };
 
 // A chunk's rows of one operand: issued to registers, staged to LDS later.
-template <typename IO, int Q, int D>
+
+template <typename IO, int Q, int D, int T>
 struct LinRows {
-    static constexpr int U = D / 8, PIECES = Q * U, N = (PIECES + kLT - 1) / kLT;
+    static constexpr int U = D / 8, PIECES = Q * U, N = (PIECES + T - 1) / T;
     lraw<IO> r[N];
-    // base: row 0 of the chunk; step: elements from one row to the next
-    __device__ __forceinline__ void load(const IO *base, int64_t step, int rows, int dim) {
+    const char *base;  // the row of the sequence's first token (last one, walking backwards)
+    uint32_t step;     // bytes from token to token
+    uint32_t at;       // byte offset of this thread's first piece in a full chunk
+    bool rev, on;
+    __device__ __forceinline__ void init(const void *rows, int64_t t0, int64_t stride, int64_t off, int dim, bool back) {
+        const int row = threadIdx.x / U, unit = threadIdx.x % U;
+        step = uint32_t(stride) * sizeof(IO);
+        rev = back;
+        base = static_cast<const char *>(rows) + (t0 * stride + off) * int64_t(sizeof(IO));
+        at = uint32_t(back ? Q - 1 - row : row) * step + unit * uint32_t(8 * sizeof(IO));
+        on = unit * 8 < dim && row < Q;
+    }
+    // the next `rows` rows; Q of them where more follow
+    __device__ __forceinline__ void load(int rows) {
+        const LinBuf b(base - (rev ? uint32_t(rows - 1) * step : 0u), uint32_t(rows) * step);
+        base += rev ? -int64_t(Q) * step : int64_t(Q) * step;
+        const uint32_t first = at - (rev ? 0u : uint32_t(Q - rows) * step), next = (rev ? 0u - step : step) * (T / U);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int piece = threadIdx.x + i * kLT, row = piece / U, unit = piece % U;
-            r[i].zero();
-            if (row < rows && unit * 8 < dim) r[i].load(base + row * step + unit * 8);
-        }
+        for (int i = 0; i < N; ++i) r[i].load(b, on ? first + i * next : kNowhere);
     }
     template <int PS>
     __device__ __forceinline__ void stage(uint16_t *m) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int piece = threadIdx.x + i * kLT;
-            if (PIECES % kLT == 0 || piece < PIECES) r[i].template stage<PS>(m + lin_at<D>(piece / U, piece % U));
+            const int piece = threadIdx.x + i * T;
+            if (PIECES % T == 0 || piece < PIECES) r[i].template stage<PS>(m + lin_at<D>(piece / U, piece % U));
         }
     }
 };
@@ -254,24 +320,26 @@ struct LinRows {
 // g^n for n >= 0 rows; g = 0 (log_decay = -inf) keeps the row itself.
 __device__ __forceinline__ float lin_power(float ld, int n) { return n > 0 ? expf(ld * float(n)) : 1.f; }
 
-// s g^n.  A slow decay is applied as s + s (g^n - 1): rounding g^n itself to
-// 24 bits would err the same way in every chunk of a long sequence.
+// s g^n, rounded once.  A slow decay is taken as s + s (g^n - 1): g^n itself,
+// rounded to 24 bits, would err the same way in every chunk of a long sequence.
 struct LinDecay {
     float f;
-    bool slow;
+    uint32_t keep; // all of s, or nothing, to add
     __device__ __forceinline__ LinDecay(float ld, double n) {
         const float x = n > 0 ? float(double(ld) * n) : 0.f;
-        slow = x > -0.5f;
-        f = slow ? expm1f(x) : expf(x);
+        f = x > -0.5f ? expm1f(x) : expf(x);
+        keep = x > -0.5f ? 0xffffffffu : 0u;
     }
-    __device__ __forceinline__ float operator()(float s) const { return slow ? fmaf(s, f, s) : s * f; }
+    __device__ __forceinline__ float operator()(float s) const {
+        return fmaf(s, f, __uint_as_float(__float_as_uint(s) & keep));
+    }
 };
 
 // Workgroup id -> work item, so that neighbouring items run on one XCD (ids go
 // round the eight XCDs) and share its L2: the scans of one head and segment,
 // and heads that share rows.
-__device__ __forceinline__ int64_t lin_xcd(int64_t id, int64_t n) {
-    const int64_t q = n / 8, r = n % 8, x = id % 8;
+__device__ __forceinline__ uint32_t lin_xcd(uint32_t id, uint32_t n) {
+    const uint32_t q = n / 8, r = n % 8, x = id % 8;
     return x * q + (x < r ? x : r) + id / 8;
 }
 
@@ -284,287 +352,315 @@ __device__ __forceinline__ void lin_tail(const LinParams &p, const LinRole &R, i
     const int64_t n = lo + (p.tokens > hi ? p.tokens - hi : 0);
     for (int64_t i = wg; i < n; i += p.tail) {
         IO *o = static_cast<IO *>(R.out) + (i < lo ? i : hi + (i - lo)) * R.ot;
-        for (int e = threadIdx.x; e < p.H * R.dz; e += kLT) io<IO>::put(o + (e / R.dz) * R.oh + e % R.dz, 0.f);
+        for (int e = threadIdx.x; e < p.H * R.dz; e += blockDim.x) io<IO>::put(o + (e / R.dz) * R.oh + e % R.dz, 0.f);
     }
+}
+
+// The launch's parameters where the kernel's arguments lie, for an index known
+// at run time: taken from the argument itself, the compiler copies it first.
+__device__ __forceinline__ const LinParams &lin_args() {
+    return *reinterpret_cast<const LinParams *>((const void *)__builtin_amdgcn_kernarg_segment_ptr());
 }
 
 // The scan.  OUT: outputs (and the final state); otherwise only the state that
 // a segment's own rows leave, for the slot of the next segment.
 template <typename IO, int DX, int DZ, bool OUT>
-__global__ __launch_bounds__(kLT) void k_linear_scan(const LinParams p) {
+__global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan(const LinParams p) {
     typedef LinCfg<IO, DX, DZ, OUT> C;
     constexpr int PL = C::PL, Q = C::Q, KS = C::KS;
     extern __shared__ __align__(16) uint16_t lds[];
     uint16_t *const xs = lds + C::XO, *const ys = lds + C::YO, *const zs = lds + C::ZO, *const sf = lds + C::SO;
 
-    const bool tail = OUT && int64_t(blockIdx.x) >= p.nwork;
-    int64_t id = tail ? int64_t(blockIdx.x) - p.nwork : lin_xcd(blockIdx.x, p.nwork);
-    const LinRole R = p.role[id % p.nroles];
-    id /= p.nroles;
+    const bool tail = OUT && blockIdx.x >= uint32_t(p.nwork);
+    uint32_t id = tail ? blockIdx.x - p.nwork : lin_xcd(blockIdx.x, p.nwork);
+    const LinRole &R = lin_args().role[id % uint32_t(p.nroles)];
+    id /= uint32_t(p.nroles);
     if (tail) {
         lin_tail<IO>(p, R, id);
         return;
     }
-    const int z0 = int(id % p.ztiles) * DZ;
-    id /= p.ztiles;
-    const int h = int(id % p.H);
-    const int64_t slot = id / p.H;
+    const int z0 = int(id % uint32_t(p.ztiles)) * DZ;
+    id /= uint32_t(p.ztiles);
+    const int h = int(id % uint32_t(p.H));
+    const int64_t slot = id / uint32_t(p.H);
     if (z0 >= R.dz) return;
 
     // the sequence of the slot, and the rows [pos, pos1) of it in scan order
     int64_t b = slot, pos = 0;
-    if (p.seglen) {
+    if (p.segbits) {
         int64_t lo = 0, hi = p.batch - 1;
         while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) / 2;
+            const int64_t mid = (lo + hi + 1) >> 1;
             if (lin_first_slot(p, mid) <= slot) lo = mid;
             else hi = mid - 1;
         }
         b = lo;
-        pos = (slot - lin_first_slot(p, b)) * p.seglen;
+        pos = (slot - lin_first_slot(p, b)) << p.segbits;
     }
     const int64_t start = lin_start(p, b), next = lin_start(p, b + 1);
     const int64_t len = next > start ? next - start : 0;
     if (pos < 0 || (pos > 0 && pos >= len)) return;          // a slot without a segment
     const bool first = pos == 0;
     int64_t pos1 = len;
-    if (p.seglen && pos + p.seglen < len) pos1 = pos + p.seglen;
+    if (p.segbits && pos + (int64_t(1) << p.segbits) < len) pos1 = pos + (int64_t(1) << p.segbits);
     const bool last = pos1 == len;
     if (!OUT && last) return;                                // nothing starts behind it
+    const float ld = p.log_decay[h];
     const int64_t pool = lin_slot(p.slots, p.nstates, b);
     if (pool == kSlotSkip) return;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r16 = lane & 15, g = lane >> 4;
+    // the wave's number as a scalar: matrix instructions ignore the lane mask, so
+    // what only some waves do has to be branched around
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), r16 = lane & 15, g = lane >> 4;
     if (pool == kSlotTaken) {
         if (OUT)
-            for (int64_t e = tid; e < (pos1 - pos) * DZ; e += kLT)
+            for (int64_t e = tid; e < (pos1 - pos) * DZ; e += C::T)
                 if (z0 + int(e % DZ) < R.dz)
                     io<IO>::put(static_cast<IO *>(R.out) + (start + pos + e / DZ) * R.ot + h * R.oh + z0 + e % DZ, __builtin_nanf(""));
         return;
     }
-    const int es = R.rev ? 0 : 1;
-    const float ld = p.log_decay[h];
+    const int64_t t0 = R.rev ? start + len - 1 - pos : start + pos; // token of the first row
+    LinRows<IO, Q, DX, C::T> xr, yr;
+    LinRows<IO, Q, DZ, C::T> zr;
+    if (OUT) xr.init(R.x, t0, R.xt, (h / R.xg) * R.xh, R.dx, R.rev);
+    yr.init(R.y, t0, R.yt, (h / R.yg) * R.yh, R.dx, R.rev);
+    zr.init(R.z, t0, R.zt, (h / R.zg) * R.zh + z0, R.dz - z0, R.rev);
+    auto load = [&](int rows) {
+        if (OUT) xr.load(rows);
+        yr.load(rows);
+        zr.load(rows);
+    };
+    int left = int(pos1 - pos); // rows to go
+    if (left > 0) load(left < Q ? left : Q);
 
-    // state: block (m, np) of this wave, fragment (mt, nt), register v is
-    // S[32 m + 8 g + 4 mt + v][z0 + 32 np + 8 (r16 / 4) + r16 % 4 + 4 nt]
-    const int mp = w % C::MW, np0 = (w / C::MW) * C::NPW;
-    floatx4 S[C::NPW][2][2];
-    const int sm0 = 32 * mp + 8 * g, sn0 = z0 + 8 * (r16 >> 2) + (r16 & 3);
-    const int64_t area = int64_t(R.dx) * R.dz;
+    const int es = R.rev ? 0 : 1;
+
+    // This wave's tiles of the state, mt0 on along x and first on (round the end)
+    // along z, and of the output, row tile rt and the tiles along z that start
+    // alike: which of them a loop over all z tiles meets is then known when it is
+    // unrolled.  State tile (i, j), register v, is
+    // S[sm0 + 4 i + v][z0 + 16 ((first + j) % NT) + r16].
+    constexpr int NT = 2 * C::NP;
+    const int mt0 = w % C::MW * C::MTW, rt = w % C::RW;
+    const int first_tile = C::NW > 1 ? w / C::MW * C::NTW : w / C::RW * C::NOT;
+    auto tile = [&](int j) { return (first_tile + j) & (NT - 1); };
+    floatx4 S[C::MTW][C::NTW];
+    const int sm0 = 32 * (mt0 >> 1) + 8 * g + 4 * (mt0 & 1);
+    const int dx = R.dx, dz = R.dz - z0;
+    const uint32_t sm = R.sm, sn = R.sn, area = uint32_t(R.dx * R.dz);
+    // every entry of this wave's tiles, with its index in an area (kNowhere / 4: none)
     auto each = [&](auto &&f) {
 #pragma unroll
-        for (int i = 0; i < C::NPW; ++i)
+        for (int j = 0; j < C::NTW; ++j) {
+            const int n = 16 * tile(j) + r16;
+            const uint32_t at = sm0 * sm + (z0 + n) * sn;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int i = 0; i < C::MTW; ++i)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int m = sm0 + 4 * mt + v, n = sn0 + 32 * (np0 + i) + 4 * nt;
-                        S[i][mt][nt][v] = f(S[i][mt][nt][v], np0 + i < C::NP && m < R.dx && n < R.dz, m * R.sm + n * R.sn);
-                    }
+                for (int v = 0; v < 4; ++v)
+                    S[i][j][v] = f(S[i][j][v], sm0 + 4 * i + v < dx && n < dz ? at + (4 * i + v) * sm : kNowhere / 4);
+        }
     };
-    bool live = false; // the state is not zero as a whole
-    if (OUT && (p.seglen ? !first || R.init : R.init != nullptr)) {
-        live = true;
-        if (p.seglen) {
-            const float *s = R.seg + (slot * p.H + h) * area;
-            each([&](float, bool in, int at) { return in ? s[at] : 0.f; });
-        } else if (R.init16) {
-            const bf16 *s = static_cast<const bf16 *>(R.init) + (pool * p.H + h) * area;
-            each([&](float, bool in, int at) { return in ? bits_to_f32(s[at].bits) : 0.f; });
+    if (OUT && (p.segbits ? !first || R.init : R.init != nullptr)) {
+        if (!p.segbits && R.init16) {
+            const LinBuf s(static_cast<const bf16 *>(R.init) + (pool * p.H + h) * int64_t(area), area * 2);
+            each([&](float, uint32_t at) { return s.get16(2 * at); });
         } else {
-            const float *s = static_cast<const float *>(R.init) + (pool * p.H + h) * area;
-            each([&](float, bool in, int at) { return in ? s[at] : 0.f; });
+            const LinBuf s((p.segbits ? R.seg + (slot * p.H + h) * int64_t(area) : static_cast<const float *>(R.init) + (pool * p.H + h) * int64_t(area)), area * 4);
+            each([&](float, uint32_t at) { return s.get(4 * at); });
         }
     } else {
-        each([](float, bool, int) { return 0.f; });
+        each([](float, uint32_t) { return 0.f; });
     }
 
-    // decay factors that every full chunk shares
-    const int rt = w % C::RW, no0 = (w / C::RW) * C::NPO;   // this wave's output rows and columns
-    float inner[2 * KS][4], from_start = 0.f;               // rows j = 16 t + 4 g + v seen from row i = 16 rt + r16
-    if (OUT) {
+    // decay factors, the same in every chunk: of row j = 16 t + 4 g + v in row
+    // i = 16 rt + r16, and at the chunk's end.  No factor is a quotient: g^n may
+    // be zero.
+    float inner[2 * KS][4], weight[2 * KS][4];
+    uint32_t upto[2] = {}; // in tile rt, the rows up to i, as masks of pairs of bf16 weights
 #pragma unroll
-        for (int t = 0; t < 2 * KS; ++t)
+    for (int v = 0; v < 4; ++v) {
+        const float diag = R.a_in * lin_power(ld, r16 - 4 * g - v);
+        upto[v >> 1] |= 4 * g + v <= r16 ? 0xffffu << 16 * (v & 1) : 0u;
+        const float over = R.a_in * lin_power(ld, 16 + r16 - 4 * g - v), end = R.a_state * lin_power(ld, 16 - es - 4 * g - v);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int n = 16 * (rt - t) + r16 - 4 * g - v;
-                inner[t][v] = n >= 0 ? R.a_in * lin_power(ld, n) : 0.f;
-            }
-        from_start = R.a_init * lin_power(ld, 16 * rt + r16 + es);
+        for (int t = 0; t < 2 * KS; ++t) {
+            inner[t][v] = t < rt ? over * lin_power(ld, 16 * (rt - 1 - t)) : diag;
+            weight[t][v] = end * lin_power(ld, 16 * (2 * KS - 1 - t));
+        }
     }
-    float weight[KS][8];                                    // rows 32 s + 16 (k / 4) + 4 g + k % 4 seen from the end
-    auto weights = [&](int rows) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                weight[s][k] = R.a_state * lin_power(ld, rows - es - (32 * s + 16 * (k >> 2) + 4 * g + (k & 3)));
-    };
-    weights(Q);
-    const LinDecay whole(ld, Q);
+    float from_start = R.a_init * lin_power(ld, 16 * rt + r16 + es);
+    LinDecay decay(ld, Q);
 
-    const int64_t sgn = R.rev ? -1 : 1, t0 = R.rev ? start + len - 1 : start;
-    const IO *xp = static_cast<const IO *>(R.x) + (t0 + sgn * pos) * R.xt + (h / R.xg) * R.xh;
-    const IO *yp = static_cast<const IO *>(R.y) + (t0 + sgn * pos) * R.yt + (h / R.yg) * R.yh;
-    const IO *zp = static_cast<const IO *>(R.z) + (t0 + sgn * pos) * R.zt + (h / R.zg) * R.zh + z0;
-    LinRows<IO, Q, DX> xr, yr;
-    LinRows<IO, Q, DZ> zr;
-    auto load = [&]() {
-        const int rows = int(pos1 - pos < Q ? pos1 - pos : Q);
-        if (OUT) xr.load(xp, sgn * R.xt, rows, R.dx);
-        yr.load(yp, sgn * R.yt, rows, R.dx);
-        zr.load(zp, sgn * R.zt, rows, R.dz - z0);
-        xp += sgn * Q * R.xt;
-        yp += sgn * Q * R.yt;
-        zp += sgn * Q * R.zt;
-    };
-    if (pos < pos1) load();
-    while (pos < pos1) {
-        const int rows = int(pos1 - pos < Q ? pos1 - pos : Q);
-        const int64_t here = t0 + sgn * pos;
-        pos += rows;
+    char *out = static_cast<char *>(R.out);
+    const int osize = C::F32 || R.out32 ? 4 : 2;
+    const uint32_t ostep = uint32_t(R.ot) * osize;
+    const uint32_t oat = uint32_t(R.rev ? Q - 1 - (16 * rt + r16) : 16 * rt + r16) * ostep + (osize == 4 ? 16 * g : 32 * (g & 1) + 16 * (g >> 1));
+    // several scans of a launch share their rows: what they write leaves the cache to those
+    const bool rev = R.rev, past = p.nroles > 1;
+    out += (t0 * R.ot + h * R.oh + z0) * osize;
+
+    while (left > 0) {
+        const int rows = left < Q ? left : Q;
+        left -= rows;
+        if (rows < Q) { // the last one
+            decay = LinDecay(ld, rows);
+            const int i = 16 * rt + r16 - (Q - rows);
+            from_start = i >= 0 ? R.a_init * lin_power(ld, i + es) : 0.f;
+        }
         if (OUT) xr.template stage<C::XP>(xs);
         yr.template stage<C::XP>(ys);
         zr.template stage<C::ZP>(zs);
-        if (OUT && live) {
+        if (OUT) {
 #pragma unroll
-            for (int i = 0; i < C::NPW; ++i)
+            for (int j = 0; j < C::NTW; ++j) {
+                // a bf16 result takes the state rounded to bf16 as operand: one
+                // rounding per term, the size of the result's own
+                uint16_t *const f = sf + (((mt0 >> 1) * NT + tile(j)) * 64 + lane) * 8;
+                float a[8];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    if (np0 + i >= C::NP) continue;
-                    float a[8];
+                for (int v = 0; v < 8; ++v) a[v] = v < 4 * C::MTW ? S[(v >> 2) % C::MTW][j][v & 3] : 0.f;
+                const lfrag<PL> q = lsplit<PL>(a);
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) a[v] = S[i][v >> 2][nt][v & 3];
-                    // a bf16 result takes the state rounded to bf16 as operand: one
-                    // rounding per term, the size of the result's own
-                    const lfrag<PL> f = lsplit<PL>(a);
-#pragma unroll
-                    for (int k = 0; k < PL; ++k)
-                        *reinterpret_cast<uint4 *>(sf + k * C::SP + (((mp * C::NP + np0 + i) * 2 + nt) * 64 + lane) * 8) =
-                            __builtin_bit_cast(uint4, f.v[k]);
+                for (int k = 0; k < PL; ++k) {
+                    const uint4 u = __builtin_bit_cast(uint4, q.v[k]);
+                    if (C::MTW == 2) *reinterpret_cast<uint4 *>(f + k * C::SP) = u;
+                    else *reinterpret_cast<uint2 *>(f + k * C::SP + 4 * (mt0 & 1)) = make_uint2(u.x, u.y);
                 }
+            }
         }
         __syncthreads();
-        if (pos < pos1) load();
+        if (left > 0) load(left < Q ? left : Q);
 
+        floatx4 O[C::NOT]; // out^T, tile j: channel z0 + 16 tile(j) + 4 g + v of row 16 rt + r16
+        lfrag<PL> pf[KS];  // weights of the chunk's rows in row 16 rt + r16
         if (OUT) {
             lfrag<PL> xf[C::MP];
 #pragma unroll
             for (int m = 0; m < C::MP; ++m) xf[m] = lin_row<PL, DX, C::XP>(xs, 16 * rt + r16, 4 * m + g);
-            // out^T, fragment nt: channel z0 + 32 np + 8 g + 4 nt + v of row 16 rt + r16
-            floatx4 O[C::NPO][2];
-#pragma unroll
-            for (int i = 0; i < C::NPO; ++i) O[i][0] = O[i][1] = floatx4{0.f, 0.f, 0.f, 0.f};
-            if (live) {
-#pragma unroll
-                for (int i = 0; i < C::NPO; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        if (no0 + i >= C::NP) continue;
-#pragma unroll
-                        for (int m = 0; m < C::MP; ++m) {
-                            lfrag<PL> f;
-#pragma unroll
-                            for (int k = 0; k < PL; ++k)
-                                f.v[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(
-                                    sf + k * C::SP + (((m * C::NP + no0 + i) * 2 + nt) * 64 + lane) * 8));
-                            O[i][nt] = lmma(O[i][nt], f, xf[m]);
-                        }
-                        O[i][nt] *= from_start;
-                    }
-            }
+            // the weights, also of the rows behind row i, which are cleared as bits:
+            // whatever they are, they must not reach it
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                if (2 * s > rt) continue; // rows behind this wave's
+                floatx4 a[2] = {};
+#pragma unroll
+                for (int m = 0; m < C::MP; ++m)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        a[u] = lmma(a[u], lin_row<PL, DX, C::XP>(ys, 32 * s + 16 * u + r16, 4 * m + g), xf[m]);
                 float pr[8];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = 2 * s + u;
-                    floatx4 a{0.f, 0.f, 0.f, 0.f};
-                    if (t <= rt) {
-#pragma unroll
-                        for (int m = 0; m < C::MP; ++m)
-                            a = lmma(a, lin_row<PL, DX, C::XP>(ys, 16 * t + r16, 4 * m + g), xf[m]);
-                    }
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        pr[4 * u + v] = t < rt || (t == rt && 4 * g + v <= r16) ? a[v] * inner[t][v] : 0.f;
-                }
+                for (int v = 0; v < 8; ++v) pr[v] = a[v >> 2][v & 3] * inner[2 * s + (v >> 2)][v & 3];
                 // the weights of a bf16 result are rounded to bf16, as above
-                const lfrag<PL> pf = lsplit<PL>(pr);
+                pf[s] = lsplit<PL>(pr);
+                const uint32_t at0 = 2 * s == rt ? ~0u : 0u, all0 = 2 * s < rt ? ~0u : 0u, at1 = 2 * s + 1 == rt ? ~0u : 0u, all1 = 2 * s + 1 < rt ? ~0u : 0u;
 #pragma unroll
-                for (int i = 0; i < C::NPO; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        if (no0 + i >= C::NP) continue;
-                        O[i][nt] = lmma(O[i][nt], lin_col<PL, DZ, C::ZP>(zs, 2 * s, no0 + i, nt, r16, g), pf);
-                    }
-            }
-            if (16 * rt + r16 < rows) {
-                const int64_t at = (here + sgn * (16 * rt + r16)) * R.ot + h * R.oh + z0 + 8 * g;
-#pragma unroll
-                for (int i = 0; i < C::NPO; ++i) {
-                    const int n = 32 * (no0 + i);
-                    if (no0 + i >= C::NP || z0 + n + 8 * g >= R.dz) continue;
-                    if (C::F32 || R.out32) {
-                        float *o = static_cast<float *>(R.out) + at + n;
-                        *reinterpret_cast<floatx4 *>(o) = O[i][0];
-                        *reinterpret_cast<floatx4 *>(o + 4) = O[i][1];
-                    } else {
-                        bf16 *o = static_cast<bf16 *>(R.out) + at + n;
-                        *reinterpret_cast<uint4 *>(o) =
-                            make_uint4(pack2_bf16(O[i][0][0], O[i][0][1]), pack2_bf16(O[i][0][2], O[i][0][3]),
-                                       pack2_bf16(O[i][1][0], O[i][1][1]), pack2_bf16(O[i][1][2], O[i][1][3]));
-                    }
+                for (int k = 0; k < PL; ++k) {
+                    const uint4 u = __builtin_bit_cast(uint4, pf[s].v[k]);
+                    pf[s].v[k] = bf16x8_from_words(u.x & ((upto[0] & at0) | all0), u.y & ((upto[1] & at0) | all0),
+                                                   u.z & ((upto[0] & at1) | all1), u.w & ((upto[1] & at1) | all1));
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < C::NOT; ++j) O[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < C::MP; ++m)
+#pragma unroll
+                for (int j = 0; j < C::NOT; ++j) {
+                    lfrag<PL> f;
+#pragma unroll
+                    for (int k = 0; k < PL; ++k)
+                        f.v[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(
+                            sf + k * C::SP + ((m * NT + tile(j)) * 64 + lane) * 8));
+                    O[j] = lmma(O[j], f, xf[m]);
+                }
+#pragma unroll
+            for (int j = 0; j < C::NOT; ++j) O[j] *= from_start;
+        }
+#pragma unroll
+        for (int i = 0; i < C::MTW; ++i)
+#pragma unroll
+            for (int j = 0; j < C::NTW; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) S[i][j][v] = decay(S[i][j][v]);
+        // the rows join the output, and, weighted by what is left of them at the
+        // chunk's end, the state
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            lfrag<3> yf[C::MTW];
+#pragma unroll
+            for (int i = 0; i < C::MTW; ++i) {
+                float a[8];
+                lunsplit(lin_ycol<PL, DX, C::XP>(ys, 2 * s, mt0 + i, r16, g), a);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a[k] *= weight[2 * s + (k >> 2)][k & 3];
+                yf[i] = lsplit<3>(a); // the state is kept to fp32 accuracy
+            }
+            // a few tiles of z at a time: the products of one plane over all of
+            // them, so that no product waits for the one before it
+            constexpr int NB = NT < 4 ? NT : 4;
+#pragma unroll
+            for (int j0 = 0; j0 < NT; j0 += NB) {
+                if (j0 >= C::NTW && (!OUT || j0 >= C::NOT)) continue;
+                lfrag<PL> zf[NB];
+#pragma unroll
+                for (int q = 0; q < NB; ++q)
+                    if (j0 + q < C::NTW || (OUT && j0 + q < C::NOT)) zf[q] = lin_zcol<PL, DZ, C::ZP>(zs, 2 * s, tile(j0 + q), r16, g);
+                if (OUT)
+                    lpairs<PL, PL>([&](auto a, auto b) {
+#pragma unroll
+                        for (int q = 0; q < NB; ++q)
+                            if (j0 + q < C::NOT)
+                                O[(j0 + q) % C::NOT] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf[q].v[a.value], pf[s].v[b.value], O[(j0 + q) % C::NOT], 0, 0, 0);
+                    });
+                lpairs<3, PL>([&](auto a, auto b) {
+#pragma unroll
+                    for (int q = 0; q < NB; ++q)
+                        if (j0 + q < C::NTW)
+#pragma unroll
+                            for (int i = 0; i < C::MTW; ++i) {
+                                floatx4 &o = S[i][(j0 + q) % C::NTW];
+                                o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(yf[i].v[a.value], zf[q].v[b.value], o, 0, 0, 0);
+                            }
+                });
             }
         }
-        // the state behind the chunk, where anything reads it
-        if (!OUT || pos < pos1 || (last && R.fin)) {
-            if (rows < Q) weights(rows);
-            if (live) {
-                const LinDecay d = rows == Q ? whole : LinDecay(ld, rows);
-                each([&](float v, bool, int) { return d(v); });
-            }
-            live = true;
+        if (OUT) {
+            const LinBuf o(out - (rev ? uint32_t(rows - 1) * ostep : 0u), uint32_t(rows) * ostep);
+            out += rev ? -int64_t(Q) * ostep : int64_t(Q) * ostep;
+            const uint32_t at = oat - (rev ? 0u : uint32_t(Q - rows) * ostep);
+            if (osize == 4) {
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                lfrag<3> yf[2];
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    float a[8];
-                    lunsplit(lin_col<PL, DX, C::XP>(ys, 2 * s, mp, mt, r16, g), a);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) a[k] *= weight[s][k];
-                    yf[mt] = lsplit<3>(a); // the state is kept to fp32 accuracy
+                for (int j = 0; j < C::NOT; ++j)
+                    o.store(16 * tile(j) + 4 * g < dz ? at + 64 * tile(j) : kNowhere, __builtin_bit_cast(uint4, O[j]), past);
+            } else if constexpr (!C::F32) {
+                // lanes of neighbouring groups swap halves of two tiles: eight
+                // neighbouring channels each
+                if (C::NOT == 2 && C::NTW == 1 && first_tile) { // the one shape whose tiles may start at an odd one
+                    const floatx4 a = O[0];
+                    O[0] = O[1 % C::NOT];
+                    O[1 % C::NOT] = a;
                 }
 #pragma unroll
-                for (int i = 0; i < C::NPW; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        if (np0 + i >= C::NP) continue;
-                        const lfrag<PL> zf = lin_col<PL, DZ, C::ZP>(zs, 2 * s, np0 + i, nt, r16, g);
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt) S[i][mt][nt] = lmma(S[i][mt][nt], yf[mt], zf);
-                    }
+                for (int j = 0; j < C::NOT; j += 2) {
+                    const int n = tile(j) & ~1;
+                    const auto a = __builtin_amdgcn_permlane16_swap(pack2_bf16(O[j][0], O[j][1]), pack2_bf16(O[j + 1][0], O[j + 1][1]), false, false);
+                    const auto b = __builtin_amdgcn_permlane16_swap(pack2_bf16(O[j][2], O[j][3]), pack2_bf16(O[j + 1][2], O[j + 1][3]), false, false);
+                    o.store(16 * n + 16 * (g & 1) + 8 * (g >> 1) < dz ? at + 32 * n : kNowhere, make_uint4(a[0], b[0], a[1], b[1]), past);
+                }
             }
         }
         __syncthreads();
     }
 
-    if (!OUT) {
-        float *s = R.seg + ((slot + 1) * p.H + h) * area;
-        each([&](float v, bool in, int at) { if (in) s[at] = v; return v; });
-    } else if (last && R.fin) {
-        if (R.fin16) {
-            bf16 *s = static_cast<bf16 *>(R.fin) + (pool * p.H + h) * area;
-            each([&](float v, bool in, int at) { if (in) s[at].bits = f32_to_bits(v); return v; });
-        } else {
-            float *s = static_cast<float *>(R.fin) + (pool * p.H + h) * area;
-            each([&](float v, bool in, int at) { if (in) s[at] = v; return v; });
-        }
+    if (OUT && (!last || !R.fin)) return;
+    if (OUT && R.fin16) {
+        const LinBuf s(static_cast<bf16 *>(R.fin) + (pool * p.H + h) * int64_t(area), area * 2);
+        each([&](float v, uint32_t at) { s.put16(2 * at, v); return v; });
+    } else {
+        const LinBuf s((OUT ? static_cast<float *>(R.fin) + (pool * p.H + h) * int64_t(area) : R.seg + ((slot + 1) * p.H + h) * int64_t(area)),
+                       area * 4);
+        each([&](float v, uint32_t at) { s.put(4 * at, v); return v; });
     }
 }
 
@@ -576,9 +672,9 @@ hipError_t launch_linear_inst(const LinParams &p, hipStream_t s) {
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, int(C::bytes));
         if (e != hipSuccess) return e;
     }
-    const int64_t grid = p.nwork + (OUT ? p.tail * p.nroles : 0);
+    const int64_t grid = int64_t(p.nwork) + (OUT ? p.tail * p.nroles : 0);
     if (grid == 0) return hipSuccess;
-    hipLaunchKernelGGL((k_linear_scan<IO, DX, DZ, OUT>), dim3(unsigned(grid)), dim3(kLT), C::bytes, s, p);
+    hipLaunchKernelGGL((k_linear_scan<IO, DX, DZ, OUT>), dim3(unsigned(grid)), dim3(C::T), C::bytes, s, p);
     return hipGetLastError();
 }
 

@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinParams p) {
     const LinRole &R = p.role[blockIdx.z];
     const int64_t b = blockIdx.x / p.H, h = blockIdx.x % p.H;
     const int64_t start = lin_start(p, b), next = lin_start(p, b + 1);
-    const int64_t len = next > start ? next - start : 0, n = (len + p.seglen - 1) / p.seglen;
+    const int64_t len = next > start ? next - start : 0, n = (len + (int64_t(1) << p.segbits) - 1) >> p.segbits;
     if (!R.init && n <= 1) return;
     const int64_t pool = lin_slot(p.slots, p.nstates, b);
     if (pool < 0) return;
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinParams p) {
     float *w = R.seg + (lin_first_slot(p, b) * p.H + h) * area + e;
     const int64_t step = p.H * area;
     if (R.init) *reinterpret_cast<floatx4 *>(w) = s;
-    const LinDecay d(p.log_decay[h], double(p.seglen));
+    const LinDecay d(p.log_decay[h], double(int64_t(1) << p.segbits));
     constexpr int U = 8; // loads in flight
     for (int64_t i = 1; i < n; i += U) {
         floatx4 a[U];
@@ -226,13 +226,13 @@ bool strides_ok(const m3_rows_t *r) {
            r->head_stride < (int64_t(1) << 40) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
 }
 // Rows to read.  Without a row the pointer is not looked at.
-bool rows_ok(const m3_rows_t *r, int64_t tokens) {
+bool rows_ok(const m3_rows_t *r, int64_t tokens, int32_t dim) {
     if (!r) return false;
-    return tokens == 0 || (r->data && aligned16(r->data) && strides_ok(r));
+    return tokens == 0 || (r->data && aligned16(r->data) && strides_ok(r) && (tokens == 1 || r->token_stride >= dim));
 }
 // Rows to write: no two may overlap, whichever axis is the outer one.
 bool out_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim) {
-    if (!rows_ok(r, tokens)) return false;
+    if (!rows_ok(r, tokens, dim)) return false;
     if (tokens == 0) return true;
     const int64_t t = r->token_stride, h = r->head_stride;
     const bool by_token = (tokens == 1 || t >= (heads - 1) * h + dim) && (heads == 1 || h >= dim);
@@ -243,14 +243,17 @@ bool out_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim) {
 // Columns of z a workgroup takes: fp32 I/O holds three planes of everything.
 int z_tile(int dz, bool f32) { return f32 ? std::min(m3::lin_tile(dz), 64) : m3::lin_tile(dz); }
 
-// Tokens per segment (0: sequences are not cut) for `scans` scans over `columns`
+// Tokens per segment, a power of two (0: sequences are not cut) for `scans` scans over `columns`
 // column tiles in one launch.
 int64_t segment(const m3_linear_shape_t *s, int scans, int columns) {
     const int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
     const int64_t per = int64_t(heads(s)) * scans * columns;
-    if (s->batch * per >= 512 || longest <= 256) return 0;
-    int64_t L = (s->tokens * per / 1024 + 63) / 64 * 64;
-    L = std::max<int64_t>(256, std::min<int64_t>(L, 4096));
+    // two workgroups a compute unit, none much longer than the others: the
+    // chip is full without cutting
+    if (longest <= 256 || (s->batch * per >= 512 && longest * s->batch < 2 * s->tokens)) return 0;
+    int64_t L = 512;
+    while (L < 4096 && L * 2048 < s->tokens * per) L *= 2;
+    while (L > 256 && s->tokens * per < L * 512) L /= 2;
     return longest > L ? L : 0;
 }
 int64_t segment_slots(const m3_linear_shape_t *s, int64_t L) { return L ? s->tokens / L + s->batch : s->batch; }
@@ -297,7 +300,7 @@ hipError_t launch_scan(LinParams p, bool f32, bool out, hipStream_t st) {
     const int dx = m3::lin_tile(p.role[0].dx), dz = z_tile(p.role[0].dz, f32);
     p.ztiles = (p.role[0].dz + dz - 1) / dz;
     for (int i = 1; i < p.nroles; ++i) p.ztiles = std::max(p.ztiles, (p.role[i].dz + dz - 1) / dz);
-    p.nwork = p.nseg * p.H * p.ztiles * p.nroles;
+    p.nwork = int32_t(p.nseg * p.H * p.ztiles * p.nroles);
     switch (dx) {
     case 32: return f32 ? m3::launch_linear_f32_32(p, dz, out, st) : m3::launch_linear_bf16_32(p, dz, out, st);
     case 64: return f32 ? m3::launch_linear_f32_64(p, dz, out, st) : m3::launch_linear_bf16_64(p, dz, out, st);
@@ -336,11 +339,13 @@ hipError_t launch_join(LinParams p, int n, hipStream_t st) {
 // One operand of a scan.
 struct Rows {
     const m3_rows_t *r;
-    int32_t heads;
+    int32_t heads, dim;
+    // the tokens' stride also bounds a chunk's rows: a single token's, which may be anything, must not cut its own
+    int64_t pitch() const { return std::max<int64_t>(r->token_stride, dim); }
 };
-void set_x(LinRole &R, const Rows &a, int32_t H) { R.x = a.r->data; R.xt = a.r->token_stride; R.xh = a.r->head_stride; R.xg = H / a.heads; }
-void set_y(LinRole &R, const Rows &a, int32_t H) { R.y = a.r->data; R.yt = a.r->token_stride; R.yh = a.r->head_stride; R.yg = H / a.heads; }
-void set_z(LinRole &R, const Rows &a, int32_t H) { R.z = a.r->data; R.zt = a.r->token_stride; R.zh = a.r->head_stride; R.zg = H / a.heads; }
+void set_x(LinRole &R, const Rows &a, int32_t H) { R.x = a.r->data; R.xt = a.pitch(); R.xh = a.r->head_stride; R.xg = H / a.heads; }
+void set_y(LinRole &R, const Rows &a, int32_t H) { R.y = a.r->data; R.yt = a.pitch(); R.yh = a.r->head_stride; R.yg = H / a.heads; }
+void set_z(LinRole &R, const Rows &a, int32_t H) { R.z = a.r->data; R.zt = a.pitch(); R.zh = a.r->head_stride; R.zg = H / a.heads; }
 
 LinParams sequences(const m3_linear_shape_t *s, const int32_t *cu, const int32_t *slots, int64_t nstates, const float *ld,
                     const Layout &w) {
@@ -353,7 +358,8 @@ LinParams sequences(const m3_linear_shape_t *s, const int32_t *cu, const int32_t
     p.slots = slots;
     p.nstates = nstates;
     p.log_decay = ld;
-    p.seglen = w.L;
+    p.each = s->tokens / s->batch;
+    while (p.segbits < 30 && w.L >> p.segbits > 1) ++p.segbits;
     p.nseg = w.slots;
     return p;
 }
@@ -395,7 +401,8 @@ m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q
     m3_status_t sc = check_shape(shape, false);
     if (sc != M3_OK) return sc;
     const int32_t H = heads(shape);
-    if (!rows_ok(q, shape->tokens) || !rows_ok(k, shape->tokens) || !rows_ok(v, shape->tokens) ||
+    if (!rows_ok(q, shape->tokens, shape->key_dim) || !rows_ok(k, shape->tokens, shape->key_dim) ||
+        !rows_ok(v, shape->tokens, shape->value_dim) ||
         !out_ok(o, shape->tokens, H, shape->value_dim))
         return M3_ERR_INVALID_ARGUMENT;
     sc = check_sequences(shape, log_decay, cu_seqlens, slots, nstates, init || final_state);
@@ -406,14 +413,14 @@ m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q
 
     LinParams p = sequences(shape, cu_seqlens, slots, nstates, log_decay, w);
     LinRole &R = p.role[0];
-    set_x(R, {q, shape->q_heads}, H);
-    set_y(R, {k, shape->k_heads}, H);
-    set_z(R, {v, shape->v_heads}, H);
+    set_x(R, {q, shape->q_heads, shape->key_dim}, H);
+    set_y(R, {k, shape->k_heads, shape->key_dim}, H);
+    set_z(R, {v, shape->v_heads, shape->value_dim}, H);
     R.out = o->data;
-    R.ot = o->token_stride;
-    R.oh = o->head_stride;
     R.dx = shape->key_dim;
     R.dz = shape->value_dim;
+    R.ot = std::max<int64_t>(o->token_stride, R.dz);
+    R.oh = o->head_stride;
     R.a_in = R.a_init = shape->scale;
     R.a_state = 1.f;
     R.init = init;
@@ -436,7 +443,8 @@ m3_status_t m3_linear_decode_step(const m3_linear_shape_t *shape, const m3_rows_
     const m3_status_t sc = check_shape(shape, true);
     if (sc != M3_OK) return sc;
     const int32_t H = heads(shape);
-    if (!rows_ok(q, shape->batch) || !rows_ok(k, shape->batch) || !rows_ok(v, shape->batch) ||
+    if (!rows_ok(q, shape->batch, shape->key_dim) || !rows_ok(k, shape->batch, shape->key_dim) ||
+        !rows_ok(v, shape->batch, shape->value_dim) ||
         !out_ok(o, shape->batch, H, shape->value_dim))
         return M3_ERR_INVALID_ARGUMENT;
     if (!log_decay || (reinterpret_cast<uintptr_t>(log_decay) & 3) || (reinterpret_cast<uintptr_t>(slots) & 3))
@@ -471,7 +479,7 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
     if (sc != M3_OK) return sc;
     const int32_t H = heads(shape), dk = shape->key_dim, dv = shape->value_dim;
     const int64_t T = shape->tokens;
-    if (!rows_ok(q, T) || !rows_ok(k, T) || !rows_ok(v, T) || !rows_ok(go, T) || !out_ok(gq, T, shape->q_heads, dk) ||
+    if (!rows_ok(q, T, dk) || !rows_ok(k, T, dk) || !rows_ok(v, T, dv) || !rows_ok(go, T, dv) || !out_ok(gq, T, shape->q_heads, dk) ||
         !out_ok(gk, T, shape->k_heads, dk) || !out_ok(gv, T, shape->v_heads, dv))
         return M3_ERR_INVALID_ARGUMENT;
     sc = check_sequences(shape, log_decay, cu_seqlens, nullptr, shape->batch, true);
@@ -483,7 +491,7 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
 
     LinParams p = sequences(shape, cu_seqlens, nullptr, shape->batch, log_decay, w);
     p.tail = cu_seqlens ? 16 : 0;
-    const Rows rq{q, shape->q_heads}, rk{k, shape->k_heads}, rv{v, shape->v_heads}, rg{go, H};
+    const Rows rq{q, shape->q_heads, shape->key_dim}, rk{k, shape->k_heads, shape->key_dim}, rv{v, shape->v_heads, shape->value_dim}, rg{go, H, dv};
     const Rows x[3] = {rg, rv, rk}, y[3] = {rv, rg, rq}, z[3] = {rk, rq, rg};
     const m3_rows_t *out[3] = {gq, gk, gv};
     const int32_t out_heads[3] = {shape->q_heads, shape->k_heads, shape->v_heads};
@@ -504,7 +512,7 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
                                 out_heads[i], H / out_heads[i], R.dz};
         } else {
             R.out = out[i]->data;
-            R.ot = out[i]->token_stride;
+            R.ot = std::max<int64_t>(out[i]->token_stride, R.dz);
             R.oh = out[i]->head_stride;
         }
         R.rev = i > 0;

@@ -15,8 +15,8 @@ from __future__ import annotations
 import torch
 
 from . import capi
-from .linear import _device, _rows
-from .mixer import _IO, _ptr, _stream
+from .linear import _device, _new_rows, _on, _rows, _stream, _workspace
+from .mixer import _IO, _ptr
 
 
 def axes_table(inv_freq: torch.Tensor, sections, interleaved: bool = False) -> torch.Tensor:
@@ -45,27 +45,39 @@ def axes_table(inv_freq: torch.Tensor, sections, interleaved: bool = False) -> t
 def _weight(w, name, d, device):
     if w is None:
         return None
-    if w.device != device or tuple(w.shape) != (d,):
-        raise ValueError(f"{name} must be [{d}] on {device}, got {tuple(w.shape)} on {w.device}")
+    _on(w, name, device)
+    if w.shape != (d,):
+        raise ValueError(f"{name} must be [{d}], got {tuple(w.shape)}")
     return _ptr(w, name, torch.float32)
+
+
+def _out(out, name, x, device):
+    if out is None:
+        return _new_rows(x.shape, x)
+    if out.shape != x.shape:
+        raise ValueError("q_out and k_out must be shaped like q and k")
+    return out, _rows(out, name, x.dtype, device)[0]
 
 
 def _common(q, k, positions, inv_freq, norm, eps, halves):
     dev, io = _device(q), q.dtype
     if io not in _IO:
         raise ValueError(f"q must be float32 or bfloat16, got {io}")
-    (rq, (b, T, hq, d)), (rk, sk) = _rows(q, "q", io, dev), _rows(k, "k", io, dev)
-    if sk[:2] != (b, T) or sk[3] != d:
+    rq, (b, T, hq, d) = _rows(q, "q", io, dev)
+    rk, (bk, Tk, hk, dk) = _rows(k, "k", io, dev)
+    if bk != b or Tk != T or dk != d:
         raise ValueError(f"q and k must share tokens and channels: {tuple(q.shape)}, {tuple(k.shape)}")
-    axes = 1 if inv_freq.dim() == 1 else inv_freq.shape[0]
-    if inv_freq.dim() not in (1, 2) or inv_freq.device != dev:
-        raise ValueError(f"inv_freq must be [n] or [axes,n] on {dev}, got {tuple(inv_freq.shape)} on {inv_freq.device}")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
-    if positions.device != dev or positions.numel() != axes * T or (axes > 1 and positions.shape[0] != axes):
-        raise ValueError(f"positions must be [{axes},{T}] on {dev}, got {tuple(positions.shape)} on {positions.device}")
-    shape = capi.m3_rotary_shape_t(T, hq, sk[2], d, 2 * inv_freq.shape[-1], axes, _IO[io],
-                                   int(positions.dtype == torch.int64), int(bool(halves)), int(bool(norm)), eps)
+    _on(inv_freq, "inv_freq", dev)
+    _on(positions, "positions", dev)
+    f, pd = inv_freq.shape, positions.dtype
+    if len(f) not in (1, 2):
+        raise ValueError(f"inv_freq must be [n] or [axes,n], got {tuple(f)}")
+    axes = 1 if len(f) == 1 else f[0]
+    if pd is not torch.int32 and pd is not torch.int64:
+        raise ValueError(f"positions must be int32 or int64, got {pd}")
+    if positions.numel() != axes * T or (axes > 1 and positions.shape[0] != axes):
+        raise ValueError(f"positions must be [{axes},{T}], got {tuple(positions.shape)}")
+    shape = capi.m3_rotary_shape_t(T, hq, hk, d, 2 * f[-1], axes, _IO[io], pd is torch.int64, bool(halves), bool(norm), eps)
     return dev, io, shape, rq, rk, _ptr(positions, "positions", None), _ptr(inv_freq, "inv_freq", torch.float32), d
 
 
@@ -75,14 +87,11 @@ def norm_rotate(q, k, positions, inv_freq, *, norm=True, eps=1e-6, q_weight=None
     ``k_out``, which may be q and k themselves).  ``q_weight`` and ``k_weight``
     [D] float32 belong to the norm; norm=False only turns."""
     dev, io, shape, rq, rk, pos, freq, d = _common(q, k, positions, inv_freq, norm, eps, halves)
-    q_out = torch.empty(q.shape, device=dev, dtype=io) if q_out is None else q_out
-    k_out = torch.empty(k.shape, device=dev, dtype=io) if k_out is None else k_out
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must be shaped like q and k")
+    q_out, ro = _out(q_out, "q_out", q, dev)
+    k_out, rko = _out(k_out, "k_out", k, dev)
     rc = capi.m3_norm_rotate(shape, rq, rk, pos, freq, _weight(q_weight, "q_weight", d, dev),
-                             _weight(k_weight, "k_weight", d, dev), _rows(q_out, "q_out", io, dev)[0],
-                             _rows(k_out, "k_out", io, dev)[0], _stream())
-    if rc != capi.M3_OK:
+                             _weight(k_weight, "k_weight", d, dev), ro, rko, _stream(dev))
+    if rc:
         raise capi.M3Error(rc, "m3_norm_rotate")
     return q_out, k_out
 
@@ -94,22 +103,17 @@ def norm_rotate_backward(q, k, positions, inv_freq, gq, gk, *, norm=True, eps=1e
     dev, io, shape, rq, rk, pos, freq, d = _common(q, k, positions, inv_freq, norm, eps, halves)
     if gq.shape != q.shape or gk.shape != k.shape:
         raise ValueError("gq and gk must be shaped like q and k")
-    need = capi.m3_norm_rotate_backward_workspace_bytes(shape)
-    if need == 0:
-        raise capi.M3Error(capi.M3_ERR_UNSUPPORTED, "m3_norm_rotate_backward_workspace_bytes")
-    if workspace is None:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
-    g = {"q": torch.empty(q.shape, device=dev, dtype=io), "k": torch.empty(k.shape, device=dev, dtype=io)}
+    wp, wn, workspace = _workspace(workspace, capi.m3_norm_rotate_backward_workspace_bytes(shape), dev,
+                                   "m3_norm_rotate_backward")
+    (dq, rdq), (dk, rdk) = _new_rows(q.shape, q), _new_rows(k.shape, k)
+    g = {"q": dq, "k": dk}
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            g[name] = torch.empty(d, device=dev, dtype=torch.float32)
+            g[name] = torch.empty((d,), device=q.device, dtype=torch.float32)
     rc = capi.m3_norm_rotate_backward(
         shape, rq, rk, pos, freq, _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev),
-        _rows(gq, "gq", io, dev)[0], _rows(gk, "gk", io, dev)[0], _rows(g["q"], "dq", io, dev)[0],
-        _rows(g["k"], "dk", io, dev)[0], *(g[n].data_ptr() if n in g else None for n in ("q_weight", "k_weight")),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream())
-    if rc != capi.M3_OK:
+        _rows(gq, "gq", io, dev)[0], _rows(gk, "gk", io, dev)[0], rdq, rdk, *(g[n].data_ptr() if n in g else None for n in ("q_weight", "k_weight")),
+        wp, wn, _stream(dev))
+    if rc:
         raise capi.M3Error(rc, "m3_norm_rotate_backward")
     return g

@@ -89,8 +89,9 @@ def test_linear_plan_and_workspace():
     # a short prompt is not cut
     assert capi.m3_linear_plan(_lshape(batch=1, tokens=200)) == (OK, 0, 0)
     assert capi.m3_linear_prefill_workspace_bytes(_lshape(batch=1, tokens=200)) == 256
-    # nor are enough sequences to fill the chip, nor one long sequence that max_seqlen says is short
-    assert capi.m3_linear_plan(_lshape(batch=256, tokens=256 * 2048))[1] == 0
+    # nor are enough like sequences to fill the chip, nor sequences that max_seqlen says are short
+    assert capi.m3_linear_plan(_lshape(batch=256, tokens=256 * 2048, max_seqlen=2048)) == (OK, 0, 0)
+    assert capi.m3_linear_plan(_lshape(batch=256, tokens=256 * 2048))[1] > 0
     assert capi.m3_linear_plan(_lshape(batch=100, tokens=20000, max_seqlen=200))[1] == 0
     # a long one is; slots of an fp32 state for every segment and sequence
     for heads, T in ((1, 100000), (8, 65536), (4, 5000)):
