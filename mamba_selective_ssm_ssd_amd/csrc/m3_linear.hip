@@ -111,6 +111,15 @@ struct LinStepParams {
     float scale;
 };
 
+// Four entries of a state.  An fp32 state is read past the cache, which the new
+// one then has for itself: 88 us against 101 us (6.1 and 5.3 TB/s) at 256 x 64
+// states of 64 x 64; a bf16 state gains nothing by it.
+__device__ __forceinline__ uint4 step_load(const float *p) {
+    const u32x4_v v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_v *>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ uint2 step_load(const bf16 *p) { return io4<bf16>::load(p); }
+
 template <typename IO, typename ST, int W>
 __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
     constexpr int L = W / 4, RP = 256 / L, NP = 128 / RP; // lanes per row, rows per pass, passes
@@ -133,7 +142,7 @@ __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
     typename io4<ST>::raw raw[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-        if (in && r0 + i * RP < p.dk) raw[i] = io4<ST>::load(st + (r0 + i * RP) * p.dv);
+        if (in && r0 + i * RP < p.dk) raw[i] = step_load(st + (r0 + i * RP) * p.dv);
     const IO *q = static_cast<const IO *>(p.q) + b * p.qt + (h / p.qg) * p.qh;
     const IO *k = static_cast<const IO *>(p.k) + b * p.kt + (h / p.kg) * p.kh;
     float qv[NP], kv[NP], v[4] = {};

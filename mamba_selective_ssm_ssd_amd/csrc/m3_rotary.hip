@@ -15,7 +15,7 @@
 namespace m3 {
 
 constexpr int kRT = 256;   // threads, four waves
-constexpr int kRows = 4;   // row sets per wave and token
+constexpr int kRows = 4;   // row sets per wave and token (twice as many where there are waves enough)
 
 struct RotRows {
     const void *x, *g;     // input rows; upstream gradient (backward)
@@ -27,25 +27,26 @@ struct RotRows {
 struct RotParams {
     RotRows r[2];          // q, k
     int64_t tokens;
-    int32_t dim, rot, axes, pos64, halves, norm;
-    float eps;
+    int32_t dim, rot, axes, pos64, norm;
+    float eps, inv_dim;
     const void *pos;
     const float *freq;
     float *part;           // backward: [workgroup][2][dim] partial gradients of the weights
 };
 
-// The channels and angles of one lane.
+// The channels and angles of one lane.  HALVES: pairs (i, i + rot / 2), across
+// the two runs; else (2i, 2i + 1), and the runs are neighbours.
+template <bool HALVES>
 struct RotLane {
     int c0, c1;            // two runs of four channels
-    bool in, turn, halves; // channels within the row; turned; pairs across the runs
+    bool in, turn;         // channels within the row; turned
     float cs[4], sn[4];
 
     __device__ __forceinline__ RotLane(const RotParams &p, int unit) {
         in = unit * 8 < p.dim;
         turn = unit * 8 < p.rot;
-        halves = p.halves != 0;
-        c0 = halves && turn ? 4 * unit : 8 * unit;
-        c1 = halves && turn ? p.rot / 2 + 4 * unit : 8 * unit + 4;
+        c0 = HALVES && turn ? 4 * unit : 8 * unit;
+        c1 = HALVES && turn ? p.rot / 2 + 4 * unit : 8 * unit + 4;
     }
     // Angles as fractions of a turn: far positions times fast frequencies lose
     // all of fp32.  position * frequency and its product with 1 / 2 pi are taken
@@ -81,7 +82,7 @@ struct RotLane {
         if (!turn) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int a = halves ? i : 2 * i, b = halves ? 4 + i : 2 * i + 1;
+            const int a = HALVES ? i : 2 * i, b = HALVES ? 4 + i : 2 * i + 1;
             const float s = back ? -sn[i] : sn[i], u = v[a], w = v[b];
             v[a] = u * cs[i] - w * s;
             v[b] = u * s + w * cs[i];
@@ -89,21 +90,44 @@ struct RotLane {
     }
 };
 
-template <typename IO>
+// A lane's eight channels as loaded.  Rows are read once: past the cache, which
+// is left to what is written.
+template <typename IO, bool HALVES>
 struct RotRaw {
-    typename io4<IO>::raw a, b;
-    __device__ __forceinline__ void load(const IO *p, const RotLane &l) { a = io4<IO>::load(p + l.c0); b = io4<IO>::load(p + l.c1); }
-    __device__ __forceinline__ void unpack(float v[8]) const { io4<IO>::unpack(a, v); io4<IO>::unpack(b, v + 4); }
+    static constexpr int W = sizeof(IO) * 2; // words
+    typedef uint32_t half __attribute__((ext_vector_type(W / 2 == 2 ? 2 : 4)));
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const IO *p, const RotLane<HALVES> &l) {
+        if constexpr (sizeof(IO) == 2 && !HALVES) {
+            const u32x4_v v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_v *>(p + l.c0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+        } else {
+            const half a = __builtin_nontemporal_load(reinterpret_cast<const half *>(p + l.c0));
+            const half b = __builtin_nontemporal_load(reinterpret_cast<const half *>(p + l.c1));
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) w[i] = a[i], w[W / 2 + i] = b[i];
+        }
+    }
+    __device__ __forceinline__ void unpack(float v[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(IO) == 4) v[i] = __uint_as_float(w[i]);
+            else v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    }
 };
-
-// One token's item j: row sets of q, then of k.
-__device__ __forceinline__ const RotRows &rot_rows(const RotParams &p, int &j) {
-    if (j < p.r[0].items) return p.r[0];
-    j -= p.r[0].items;
-    return p.r[1];
+template <typename IO, bool HALVES>
+__device__ __forceinline__ void rot_store(IO *p, const RotLane<HALVES> &l, const float v[8]) {
+    if constexpr (sizeof(IO) == 2 && !HALVES) {
+        *reinterpret_cast<uint4 *>(p + l.c0) = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
+    } else {
+        io<IO>::store4(p + l.c0, v);
+        io<IO>::store4(p + l.c1, v + 4);
+    }
 }
 
-template <typename IO, int LPR>
+template <typename IO, int LPR, bool HALVES, int NR>
 __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
     constexpr int RPW = 64 / LPR;
     const int lane = threadIdx.x & 63, unit = lane % LPR, sub = lane / LPR;
@@ -114,13 +138,13 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
     const bool is_q = j < p.r[0].items;
     if (!is_q) j -= p.r[0].items;
     const RotRows R = is_q ? p.r[0] : p.r[1];
-    RotLane l(p, unit);
-    const int h0 = j * kRows * RPW + sub;
+    RotLane<HALVES> l(p, unit);
+    const int h0 = j * NR * RPW + sub;
     const IO *x = static_cast<const IO *>(R.x) + token * R.xt;
     IO *o = static_cast<IO *>(R.out) + token * R.ot;
-    RotRaw<IO> raw[kRows];
+    RotRaw<IO, HALVES> raw[NR];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+    for (int i = 0; i < NR; ++i)
         if (l.in && h0 + i * RPW < R.heads) raw[i].load(x + (h0 + i * RPW) * R.xh, l);
     float w[8];
 #pragma unroll
@@ -131,7 +155,7 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
     }
     l.angles(p, unit, token);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < NR; ++i) {
         const bool on = l.in && h0 + i * RPW < R.heads;
         float v[8] = {};
         if (on) raw[i].unpack(v);
@@ -139,15 +163,12 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
             float ss = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) / float(p.dim) + p.eps);
+            const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<LPR>(ss), p.inv_dim, p.eps));
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] *= r * w[c];
         }
         l.rotate(v, false);
-        if (on) {
-            io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c0, v);
-            io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c1, v + 4);
-        }
+        if (on) rot_store(o + (h0 + i * RPW) * R.oh, l, v);
     }
 }
 
@@ -155,12 +176,12 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
 //     dw = sum gn r x,    dx = r w gn - (r^3 / dim) x sum(x w gn).
 // Workgroups walk the items with a fixed stride and keep their share of dw in
 // registers; k_norm_rotate_sum adds the shares in a fixed order.
-template <typename IO, int LPR>
-__global__ __launch_bounds__(kRT) void k_norm_rotate_backward(const RotParams p) {
+template <typename IO, int LPR, bool HALVES>
+__global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams p) {
     constexpr int RPW = 64 / LPR, NW = kRT / 64;
     __shared__ float part[NW][LPR * 8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, unit = lane % LPR, sub = lane / LPR;
-    RotLane l(p, unit);
+    RotLane<HALVES> l(p, unit);
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         const RotRows R = kind ? p.r[1] : p.r[0];
@@ -178,7 +199,7 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate_backward(const RotParams p)
             const IO *x = static_cast<const IO *>(R.x) + token * R.xt;
             const IO *g = static_cast<const IO *>(R.g) + token * R.gt;
             IO *o = static_cast<IO *>(R.out) + token * R.ot;
-            RotRaw<IO> rx[kRows], rg[kRows];
+            RotRaw<IO, HALVES> rx[kRows], rg[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
                 if (l.in && h0 + i * RPW < R.heads) {
@@ -197,21 +218,18 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate_backward(const RotParams p)
                     if (on) rx[i].unpack(v);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
-                    const float r = rsqrtf(row_sum<LPR>(ss) / float(p.dim) + p.eps);
+                    const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<LPR>(ss), p.inv_dim, p.eps));
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         dw[c] = fmaf(a[c] * r, v[c], dw[c]);
                         a[c] *= w[c];
                         dot = fmaf(v[c], a[c], dot);
                     }
-                    const float m = row_sum<LPR>(dot) / float(p.dim) * r * r;
+                    const float m = row_sum<LPR>(dot) * p.inv_dim * (r * r);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) a[c] = r * (a[c] - m * v[c]);
                 }
-                if (on) {
-                    io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c0, a);
-                    io<IO>::store4(o + (h0 + i * RPW) * R.oh + l.c1, a + 4);
-                }
+                if (on) rot_store(o + (h0 + i * RPW) * R.oh, l, a);
             }
         }
         if (!R.w) continue;
@@ -237,22 +255,27 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate_backward(const RotParams p)
     }
 }
 
-// Sum of the workgroups' shares: 16 channels by 64 strips of workgroups.
+// Sum of the workgroups' shares, four channels of one weight per workgroup: a
+// share to a thread, then the threads of a wave and the waves in pairs.
 __global__ __launch_bounds__(1024) void k_norm_rotate_sum(const float *part, int n, int dim, float *dq, float *dk) {
-    __shared__ float s[64][17];
-    const int c = blockIdx.x * 16 + threadIdx.x % 16, strip = threadIdx.x / 16, kind = blockIdx.y;
+    __shared__ floatx4 s[16];
+    const int c = blockIdx.x * 4, kind = blockIdx.y;
     float *out = kind ? dk : dq;
     if (!out) return;
-    float a = 0.f;
-    if (c < dim)
-        for (int i = strip; i < n; i += 64) a += part[(int64_t(i) * 2 + kind) * dim + c];
-    s[strip][threadIdx.x % 16] = a;
+    floatx4 a{0.f, 0.f, 0.f, 0.f};
+    for (int i = threadIdx.x; i < n; i += 1024) a += *reinterpret_cast<const floatx4 *>(part + (int64_t(i) * 2 + kind) * dim + c);
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a[v] += __shfl_xor(a[v], m);
+    if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = a;
     __syncthreads();
-    for (int m = 32; m > 0; m >>= 1) {
-        if (strip < m) s[strip][threadIdx.x % 16] += s[strip + m][threadIdx.x % 16];
-        __syncthreads();
+    if (threadIdx.x < 4) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) t += s[w][threadIdx.x];
+        out[c + threadIdx.x] = t;
     }
-    if (strip == 0 && c < dim) out[c] = s[0][threadIdx.x];
 }
 
 // Lanes of a row: the power of two that holds dim / 8.
@@ -262,24 +285,37 @@ constexpr int rot_lanes(int dim) {
     return n;
 }
 
-template <typename IO, int LPR>
-hipError_t launch_rotary(const RotParams &p, int64_t grid, bool back, hipStream_t s) {
-    if (back) hipLaunchKernelGGL((k_norm_rotate_backward<IO, LPR>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
-    else hipLaunchKernelGGL((k_norm_rotate<IO, LPR>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
+template <typename IO, int LPR, bool HALVES>
+hipError_t launch_rotary(RotParams &p, int64_t grid, bool back, hipStream_t s) {
+    if (back) {
+        hipLaunchKernelGGL((k_norm_rotate_backward<IO, LPR, HALVES>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
+        return hipGetLastError();
+    }
+    // twice the rows for a wave's angles where that still leaves eight waves a SIMD
+    const bool two = grid >= 2 * 2048;
+    if (two)
+        for (RotRows &r : p.r) r.items = (r.heads + 2 * kRows * (64 / LPR) - 1) / (2 * kRows * (64 / LPR));
+    const int64_t n = (p.tokens * (p.r[0].items + p.r[1].items) + 3) / 4;
+    if (two) hipLaunchKernelGGL((k_norm_rotate<IO, LPR, HALVES, 2 * kRows>), dim3(unsigned(n)), dim3(kRT), 0, s, p);
+    else hipLaunchKernelGGL((k_norm_rotate<IO, LPR, HALVES, kRows>), dim3(unsigned(n)), dim3(kRT), 0, s, p);
     return hipGetLastError();
 }
 
-template <typename IO>
-hipError_t launch_rotary_io(const RotParams &p, int64_t grid, bool back, hipStream_t s) {
+template <typename IO, bool HALVES>
+hipError_t launch_rotary_lanes(RotParams &p, int64_t grid, bool back, hipStream_t s) {
     switch (rot_lanes(p.dim)) {
-    case 1: return launch_rotary<IO, 1>(p, grid, back, s);
-    case 2: return launch_rotary<IO, 2>(p, grid, back, s);
-    case 4: return launch_rotary<IO, 4>(p, grid, back, s);
-    case 8: return launch_rotary<IO, 8>(p, grid, back, s);
-    case 16: return launch_rotary<IO, 16>(p, grid, back, s);
-    case 32: return launch_rotary<IO, 32>(p, grid, back, s);
+    case 1: return launch_rotary<IO, 1, HALVES>(p, grid, back, s);
+    case 2: return launch_rotary<IO, 2, HALVES>(p, grid, back, s);
+    case 4: return launch_rotary<IO, 4, HALVES>(p, grid, back, s);
+    case 8: return launch_rotary<IO, 8, HALVES>(p, grid, back, s);
+    case 16: return launch_rotary<IO, 16, HALVES>(p, grid, back, s);
+    case 32: return launch_rotary<IO, 32, HALVES>(p, grid, back, s);
     }
     return hipErrorInvalidValue;
+}
+template <typename IO>
+hipError_t launch_rotary_io(RotParams &p, bool halves, int64_t grid, bool back, hipStream_t s) {
+    return halves ? launch_rotary_lanes<IO, true>(p, grid, back, s) : launch_rotary_lanes<IO, false>(p, grid, back, s);
 }
 
 } // namespace m3
@@ -318,11 +354,14 @@ int32_t items(const m3_rotary_shape_t *s, int32_t heads) {
     return (heads + set - 1) / set;
 }
 
-// Workgroups of the gradients: four per compute unit at most, so that the
-// partial sums of the weights stay few.
+// Workgroups of the gradients: at most the four per compute unit that are
+// resident at once (128 registers), so that they share the rows evenly and leave
+// few partial sums.  Twice as many took as long (76 us at 8192 x 128 x 64) and
+// their sum 1 us more.
+constexpr int64_t kBackGrid = 1024;
 int64_t backward_grid(const m3_rotary_shape_t *s) {
     const int64_t n = s->tokens * std::max(items(s, s->q_heads), items(s, s->k_heads));
-    return std::max<int64_t>(1, std::min<int64_t>((n + 3) / 4, 1024));
+    return std::max<int64_t>(1, std::min<int64_t>((n + 3) / 4, kBackGrid));
 }
 
 m3::RotParams params(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_rows_t *k, const void *pos,
@@ -344,9 +383,9 @@ m3::RotParams params(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_ro
     p.rot = s->rot;
     p.axes = s->axes;
     p.pos64 = s->pos_int64;
-    p.halves = s->halves;
     p.norm = s->norm;
     p.eps = s->eps;
+    p.inv_dim = 1.f / float(s->dim);
     p.pos = pos;
     p.freq = freq;
     return p;
@@ -377,10 +416,10 @@ m3_status_t m3_norm_rotate(const m3_rotary_shape_t *shape, const m3_rows_t *q, c
         !rows_ok(q_out, T, shape->q_heads, shape->dim, true) || !rows_ok(k_out, T, shape->k_heads, shape->dim, true))
         return M3_ERR_INVALID_ARGUMENT;
     if (T == 0) return M3_OK;
-    const m3::RotParams p = params(shape, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out);
+    m3::RotParams p = params(shape, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out);
     const int64_t grid = (T * (p.r[0].items + p.r[1].items) + 3) / 4;
-    const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, grid, false, stream)
-                                                         : m3::launch_rotary_io<m3::bf16>(p, grid, false, stream);
+    const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, shape->halves, grid, false, stream)
+                                                         : m3::launch_rotary_io<m3::bf16>(p, shape->halves, grid, false, stream);
     return e == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
 
@@ -412,11 +451,11 @@ m3_status_t m3_norm_rotate_backward(const m3_rotary_shape_t *shape, const m3_row
     if (shape->k_heads) { p.r[1].g = gk->data; p.r[1].gt = gk->token_stride; p.r[1].gh = gk->head_stride; }
     p.part = static_cast<float *>(workspace);
     const int64_t grid = backward_grid(shape);
-    const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, grid, true, stream)
-                                                         : m3::launch_rotary_io<m3::bf16>(p, grid, true, stream);
+    const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, shape->halves, grid, true, stream)
+                                                         : m3::launch_rotary_io<m3::bf16>(p, shape->halves, grid, true, stream);
     if (e != hipSuccess) return M3_ERR_HIP;
     if (dq_weight || dk_weight) {
-        hipLaunchKernelGGL(m3::k_norm_rotate_sum, dim3(unsigned((shape->dim + 15) / 16), 2), dim3(1024), 0, stream,
+        hipLaunchKernelGGL(m3::k_norm_rotate_sum, dim3(unsigned(shape->dim / 4), 2), dim3(1024), 0, stream,
                            p.part, int(grid), shape->dim, dq_weight, dk_weight);
         if (hipGetLastError() != hipSuccess) return M3_ERR_HIP;
     }
