@@ -37,12 +37,13 @@ struct LinRole {
     void *fin;               // state pool, or null: not written
     int32_t init16, fin16;   // the pools' entries are bf16
     int32_t sm, sn;          // strides of the state's two axes (pools and seg alike)
-    float *seg;              // [segment slot][H][dx dz] fp32: state at the start of each segment
+    float *seg;              // [segment slot][H][dx dz] fp32, for the start of each segment of a cut sequence
 };
 
 struct LinParams {
     LinRole role[3];
     int32_t nroles, H, ztiles;
+    int32_t hg, group;       // heads that share rows; workgroups that do: hg x ztiles x nroles
     int32_t tail;            // extra workgroups per scan that zero the rows outside every sequence
     int32_t nwork;           // workgroups without the tail
     int64_t batch, tokens, each; // each: tokens of a sequence without cu
@@ -51,6 +52,7 @@ struct LinParams {
     int64_t nstates;
     const float *log_decay;
     int32_t segbits;         // log2 of the tokens per segment, 0: sequences are not cut
+    int32_t fold;            // slots hold what each segment leaves, not yet joined
     int64_t nseg;            // segment slots (batch when not cut)
 };
 
@@ -282,12 +284,24 @@ struct lraw<float> {
 };
 
 // A chunk's rows of one operand: issued to registers, staged to LDS later.
+template <typename IO, int Q, int D, int T>
+struct LinRegs {
+    static constexpr int U = D / 8, PIECES = Q * U, N = (PIECES + T - 1) / T;
+    lraw<IO> r[N];
+    template <int PS>
+    __device__ __forceinline__ void stage(uint16_t *m) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int piece = threadIdx.x + i * T;
+            if (PIECES % T == 0 || piece < PIECES) r[i].template stage<PS>(m + lin_at<D>(piece / U, piece % U));
+        }
+    }
+};
 
 template <typename IO, int Q, int D, int T>
 struct LinRows {
-    static constexpr int U = D / 8, PIECES = Q * U, N = (PIECES + T - 1) / T;
-    lraw<IO> r[N];
-    const char *base;  // the row of the sequence's first token (last one, walking backwards)
+    static constexpr int U = D / 8;
+    const char *base;  // the row of the next chunk's first token (walking backwards: last)
     uint32_t step;     // bytes from token to token
     uint32_t at;       // byte offset of this thread's first piece in a full chunk
     bool rev, on;
@@ -300,25 +314,19 @@ struct LinRows {
         on = unit * 8 < dim && row < Q;
     }
     // the next `rows` rows; Q of them where more follow
-    __device__ __forceinline__ void load(int rows) {
+    __device__ __forceinline__ void load(LinRegs<IO, Q, D, T> &to, int rows) {
         const LinBuf b(base - (rev ? uint32_t(rows - 1) * step : 0u), uint32_t(rows) * step);
         base += rev ? -int64_t(Q) * step : int64_t(Q) * step;
         const uint32_t first = at - (rev ? 0u : uint32_t(Q - rows) * step), next = (rev ? 0u - step : step) * (T / U);
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i].load(b, on ? first + i * next : kNowhere);
-    }
-    template <int PS>
-    __device__ __forceinline__ void stage(uint16_t *m) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int piece = threadIdx.x + i * T;
-            if (PIECES % T == 0 || piece < PIECES) r[i].template stage<PS>(m + lin_at<D>(piece / U, piece % U));
-        }
+        for (int i = 0; i < to.N; ++i) to.r[i].load(b, on ? first + i * next : kNowhere);
     }
 };
 
-// g^n for n >= 0 rows; g = 0 (log_decay = -inf) keeps the row itself.
-__device__ __forceinline__ float lin_power(float ld, int n) { return n > 0 ? expf(ld * float(n)) : 1.f; }
+// g^n, 1 for n <= 0 rows: g = 0 (log_decay = -inf) keeps the row itself.  ld2 is
+// log_decay / log 2; the exponent is off by two roundings of itself, 2^-22 of a
+// factor of e^-2 and less where the factor is nearer to one.
+__device__ __forceinline__ float lin_power(float ld2, int n) { return n > 0 ? __builtin_amdgcn_exp2f(ld2 * float(n)) : 1.f; }
 
 // s g^n, rounded once.  A slow decay is taken as s + s (g^n - 1): g^n itself,
 // rounded to 24 bits, would err the same way in every chunk of a long sequence.
@@ -335,13 +343,25 @@ struct LinDecay {
     }
 };
 
-// Workgroup id -> work item, so that neighbouring items run on one XCD (ids go
-// round the eight XCDs) and share its L2: the scans of one head and segment,
-// and heads that share rows.
-__device__ __forceinline__ uint32_t lin_xcd(uint32_t id, uint32_t n) {
-    const uint32_t q = n / 8, r = n % 8, x = id % 8;
-    return x * q + (x < r ? x : r) + id / 8;
-}
+// The decay of a state chunk by chunk, one product an entry.  g^n rounded to 24
+// bits would err the same way in every chunk of a long sequence; here each
+// chunk's factor also makes up for the rounding of those before it, so that the
+// product of all of them is right to 24 bits.
+struct LinDecays {
+    double exact, back, owed; // g^Q, 1 / g^Q, what the product of the factors so far lacks
+    __device__ __forceinline__ LinDecays(float ld, int n) : exact(power(ld, n)), owed(1.0) { back = exact > 1e-30 ? 1.0 / exact : 0.0; }
+    static __device__ __forceinline__ double power(float ld, int n) {
+        const float x = ld * float(n); // n is a power of two, or the last chunk's
+        return x > -0.5f ? 1.0 + double(expm1f(x)) : double(expf(x));
+    }
+    __device__ __forceinline__ float next() {
+        const double t = owed * exact;
+        const float f = float(t);
+        owed = fma(t - double(f), back, 1.0);
+        return f;
+    }
+    __device__ __forceinline__ float last(float ld, int n) const { return float(owed * power(ld, n)); }
+};
 
 // Zeroes a gradient's rows of tokens outside every sequence (the fp32 parts of
 // a shared row are left to their sum).
@@ -363,26 +383,32 @@ __device__ __forceinline__ const LinParams &lin_args() {
 }
 
 // The scan.  OUT: outputs (and the final state); otherwise only the state that
-// a segment's own rows leave, for the slot of the next segment.
-template <typename IO, int DX, int DZ, bool OUT>
-__global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan(const LinParams p) {
+// a segment's own rows leave, for the slot of the next segment.  UP: planes of
+// the weighted y that join the state; three keep it to fp32 accuracy, two (2^-17)
+// do where it is only rounded to bf16 and not handed out.
+template <typename IO, int DX, int DZ, bool OUT, int UP>
+__global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k_linear_scan(const LinParams p) {
     typedef LinCfg<IO, DX, DZ, OUT> C;
     constexpr int PL = C::PL, Q = C::Q, KS = C::KS;
     extern __shared__ __align__(16) uint16_t lds[];
     uint16_t *const xs = lds + C::XO, *const ys = lds + C::YO, *const zs = lds + C::ZO, *const sf = lds + C::SO;
 
+    // Workgroups that share rows (the scans, column tiles and heads of a group)
+    // follow each other on one XCD, whose L2 they share; ids go round the eight
+    // XCDs, and so do the groups: segments and heads differ in work.
     const bool tail = OUT && blockIdx.x >= uint32_t(p.nwork);
-    uint32_t id = tail ? blockIdx.x - p.nwork : lin_xcd(blockIdx.x, p.nwork);
+    uint32_t id = tail ? blockIdx.x - p.nwork : blockIdx.x / 8 % uint32_t(p.group);
     const LinRole &R = lin_args().role[id % uint32_t(p.nroles)];
     id /= uint32_t(p.nroles);
     if (tail) {
         lin_tail<IO>(p, R, id);
         return;
     }
+    const uint32_t unit = blockIdx.x / 8 / uint32_t(p.group) * 8 + blockIdx.x % 8, units = uint32_t(p.H / p.hg);
     const int z0 = int(id % uint32_t(p.ztiles)) * DZ;
-    id /= uint32_t(p.ztiles);
-    const int h = int(id % uint32_t(p.H));
-    const int64_t slot = id / uint32_t(p.H);
+    const int h = int(unit % units * p.hg + id / uint32_t(p.ztiles));
+    const int64_t slot = unit / units;
+    if (slot >= p.nseg) return;
     if (z0 >= R.dz) return;
 
     // the sequence of the slot, and the rows [pos, pos1) of it in scan order
@@ -411,7 +437,8 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
 
     // the wave's number as a scalar: matrix instructions ignore the lane mask, so
     // what only some waves do has to be branched around
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), r16 = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     if (pool == kSlotTaken) {
         if (OUT)
             for (int64_t e = tid; e < (pos1 - pos) * DZ; e += C::T)
@@ -425,15 +452,24 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
     if (OUT) xr.init(R.x, t0, R.xt, (h / R.xg) * R.xh, R.dx, R.rev);
     yr.init(R.y, t0, R.yt, (h / R.yg) * R.yh, R.dx, R.rev);
     zr.init(R.z, t0, R.zt, (h / R.zg) * R.zh + z0, R.dz - z0, R.rev);
-    auto load = [&](int rows) {
-        if (OUT) xr.load(rows);
-        yr.load(rows);
-        zr.load(rows);
+    // rows on their way: a chunk's, or two chunks' where there is little else to do
+    constexpr int AHEAD = 1;
+    LinRegs<IO, Q, DX, C::T> xq[1], yq[AHEAD];
+    LinRegs<IO, Q, DZ, C::T> zq[AHEAD];
+    int left = int(pos1 - pos), ahead = left; // rows to go, and to load
+    auto load = [&](int set) __attribute__((always_inline)) {
+        if (ahead <= 0) return;
+        const int rows = ahead < Q ? ahead : Q;
+        if (OUT) xr.load(xq[0], rows);
+        yr.load(yq[set], rows);
+        zr.load(zq[set], rows);
+        ahead -= rows;
     };
-    int left = int(pos1 - pos); // rows to go
-    if (left > 0) load(left < Q ? left : Q);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load(i);
 
     const int es = R.rev ? 0 : 1;
+    const float ld2 = ld * 1.44269504f;
 
     // This wave's tiles of the state, mt0 on along x and first on (round the end)
     // along z, and of the output, row tile rt and the tiles along z that start
@@ -443,13 +479,13 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
     constexpr int NT = 2 * C::NP;
     const int mt0 = w % C::MW * C::MTW, rt = w % C::RW;
     const int first_tile = C::NW > 1 ? w / C::MW * C::NTW : w / C::RW * C::NOT;
-    auto tile = [&](int j) { return (first_tile + j) & (NT - 1); };
+    auto tile = [&](int j) __attribute__((always_inline)) { return (first_tile + j) & (NT - 1); };
     floatx4 S[C::MTW][C::NTW];
     const int sm0 = 32 * (mt0 >> 1) + 8 * g + 4 * (mt0 & 1);
     const int dx = R.dx, dz = R.dz - z0;
     const uint32_t sm = R.sm, sn = R.sn, area = uint32_t(R.dx * R.dz);
     // every entry of this wave's tiles, with its index in an area (kNowhere / 4: none)
-    auto each = [&](auto &&f) {
+    auto each = [&](auto &&f) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < C::NTW; ++j) {
             const int n = 16 * tile(j) + r16;
@@ -461,13 +497,34 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
                     S[i][j][v] = f(S[i][j][v], sm0 + 4 * i + v < dx && n < dz ? at + (4 * i + v) * sm : kNowhere / 4);
         }
     };
-    if (OUT && (p.segbits ? !first || R.init : R.init != nullptr)) {
-        if (!p.segbits && R.init16) {
-            const LinBuf s(static_cast<const bf16 *>(R.init) + (pool * p.H + h) * int64_t(area), area * 2);
+    // The state to start from.  A sequence that is not cut has it in its pool; of a
+    // cut one the first segment's pass takes it along and leaves a copy in the
+    // first slot, so that the last segment's may write the pool.  The slots behind
+    // hold what the segments left, each without those before it where they are
+    // still to be folded.
+    const bool cut = p.segbits && !(first && last);
+    const int64_t seg_at = (slot * p.H + h) * int64_t(area);
+    if (OUT && cut && (!first || R.init)) {
+        const int64_t from = OUT && p.fold && !first ? (pos >> p.segbits) - 1 : 0; // slots before this one to fold in
+        LinBuf s0(R.seg + seg_at - from * p.H * int64_t(area), area * 4);
+        each([&](float, uint32_t at) { return s0.get(4 * at); });
+        const LinDecay d(ld, double(int64_t(1) << p.segbits));
+        for (int64_t i = from - 1; i >= 0; --i) {
+            const LinBuf s(R.seg + seg_at - i * p.H * int64_t(area), area * 4);
+            each([&](float v, uint32_t at) { return d(v) + s.get(4 * at); });
+        }
+    } else if (R.init && first) {
+        const int64_t at0 = (pool * p.H + h) * int64_t(area);
+        if (R.init16) {
+            const LinBuf s(static_cast<const bf16 *>(R.init) + at0, area * 2);
             each([&](float, uint32_t at) { return s.get16(2 * at); });
         } else {
-            const LinBuf s((p.segbits ? R.seg + (slot * p.H + h) * int64_t(area) : static_cast<const float *>(R.init) + (pool * p.H + h) * int64_t(area)), area * 4);
+            const LinBuf s(static_cast<const float *>(R.init) + at0, area * 4);
             each([&](float, uint32_t at) { return s.get(4 * at); });
+        }
+        if (!OUT) {
+            const LinBuf s(R.seg + seg_at, area * 4);
+            each([&](float v, uint32_t at) { s.put(4 * at, v); return v; });
         }
     } else {
         each([](float, uint32_t) { return 0.f; });
@@ -480,37 +537,40 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
     uint32_t upto[2] = {}; // in tile rt, the rows up to i, as masks of pairs of bf16 weights
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        const float diag = R.a_in * lin_power(ld, r16 - 4 * g - v);
+        const float diag = R.a_in * lin_power(ld2, r16 - 4 * g - v);
         upto[v >> 1] |= 4 * g + v <= r16 ? 0xffffu << 16 * (v & 1) : 0u;
-        const float over = R.a_in * lin_power(ld, 16 + r16 - 4 * g - v), end = R.a_state * lin_power(ld, 16 - es - 4 * g - v);
+        const float over = R.a_in * lin_power(ld2, 16 + r16 - 4 * g - v), end = R.a_state * lin_power(ld2, 16 - es - 4 * g - v);
 #pragma unroll
         for (int t = 0; t < 2 * KS; ++t) {
-            inner[t][v] = t < rt ? over * lin_power(ld, 16 * (rt - 1 - t)) : diag;
-            weight[t][v] = end * lin_power(ld, 16 * (2 * KS - 1 - t));
+            inner[t][v] = t < rt ? over * lin_power(ld2, 16 * (rt - 1 - t)) : diag;
+            weight[t][v] = end * lin_power(ld2, 16 * (2 * KS - 1 - t));
         }
     }
-    float from_start = R.a_init * lin_power(ld, 16 * rt + r16 + es);
-    LinDecay decay(ld, Q);
-
+    float from_start = R.a_init * lin_power(ld2, 16 * rt + r16 + es);
+    LinDecays decays(ld, Q);
     char *out = static_cast<char *>(R.out);
     const int osize = C::F32 || R.out32 ? 4 : 2;
     const uint32_t ostep = uint32_t(R.ot) * osize;
     const uint32_t oat = uint32_t(R.rev ? Q - 1 - (16 * rt + r16) : 16 * rt + r16) * ostep + (osize == 4 ? 16 * g : 32 * (g & 1) + 16 * (g >> 1));
-    // several scans of a launch share their rows: what they write leaves the cache to those
-    const bool rev = R.rev, past = p.nroles > 1;
+    // several scans of a launch share their rows: what they write leaves the cache
+    // to those, but for the parts that are read again next
+    const bool rev = R.rev, past = p.nroles > 1 && !R.out32;
     out += (t0 * R.ot + h * R.oh + z0) * osize;
 
-    while (left > 0) {
+    auto chunk = [&](int set) __attribute__((always_inline)) {
         const int rows = left < Q ? left : Q;
         left -= rows;
-        if (rows < Q) { // the last one
-            decay = LinDecay(ld, rows);
+        float decay;
+        if (rows == Q) {
+            decay = decays.next();
+        } else { // the last one
+            decay = decays.last(ld, rows);
             const int i = 16 * rt + r16 - (Q - rows);
-            from_start = i >= 0 ? R.a_init * lin_power(ld, i + es) : 0.f;
+            from_start = i >= 0 ? R.a_init * lin_power(ld2, i + es) : 0.f;
         }
-        if (OUT) xr.template stage<C::XP>(xs);
-        yr.template stage<C::XP>(ys);
-        zr.template stage<C::ZP>(zs);
+        if (OUT) xq[0].template stage<C::XP>(xs);
+        yq[set].template stage<C::XP>(ys);
+        zq[set].template stage<C::ZP>(zs);
         if (OUT) {
 #pragma unroll
             for (int j = 0; j < C::NTW; ++j) {
@@ -530,7 +590,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
             }
         }
         __syncthreads();
-        if (left > 0) load(left < Q ? left : Q);
+        load(set);
 
         floatx4 O[C::NOT]; // out^T, tile j: channel z0 + 16 tile(j) + 4 g + v of row 16 rt + r16
         lfrag<PL> pf[KS];  // weights of the chunk's rows in row 16 rt + r16
@@ -582,19 +642,19 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
 #pragma unroll
             for (int j = 0; j < C::NTW; ++j)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) S[i][j][v] = decay(S[i][j][v]);
+                for (int v = 0; v < 4; ++v) S[i][j][v] *= decay;
         // the rows join the output, and, weighted by what is left of them at the
-        // chunk's end, the state
+        // chunk's end, in UP planes, the state
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            lfrag<3> yf[C::MTW];
+            lfrag<UP> yf[C::MTW];
 #pragma unroll
             for (int i = 0; i < C::MTW; ++i) {
                 float a[8];
                 lunsplit(lin_ycol<PL, DX, C::XP>(ys, 2 * s, mt0 + i, r16, g), a);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) a[k] *= weight[2 * s + (k >> 2)][k & 3];
-                yf[i] = lsplit<3>(a); // the state is kept to fp32 accuracy
+                yf[i] = lsplit<UP>(a);
             }
             // a few tiles of z at a time: the products of one plane over all of
             // them, so that no product waits for the one before it
@@ -613,7 +673,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
                             if (j0 + q < C::NOT)
                                 O[(j0 + q) % C::NOT] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf[q].v[a.value], pf[s].v[b.value], O[(j0 + q) % C::NOT], 0, 0, 0);
                     });
-                lpairs<3, PL>([&](auto a, auto b) {
+                lpairs<UP, PL>([&](auto a, auto b) {
 #pragma unroll
                     for (int q = 0; q < NB; ++q)
                         if (j0 + q < C::NTW)
@@ -651,6 +711,10 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
             }
         }
         __syncthreads();
+    };
+    while (left > 0) {
+        chunk(0);
+        if (AHEAD == 2 && left > 0) chunk(1);
     }
 
     if (OUT && (!last || !R.fin)) return;
@@ -664,18 +728,28 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), 2) void k_linear_scan
     }
 }
 
-template <typename IO, int DX, int DZ, bool OUT>
-hipError_t launch_linear_inst(const LinParams &p, hipStream_t s) {
+template <typename IO, int DX, int DZ, bool OUT, int UP>
+hipError_t launch_linear_planes(const LinParams &p, hipStream_t s) {
     typedef LinCfg<IO, DX, DZ, OUT> C;
     if (C::bytes > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_linear_scan<IO, DX, DZ, OUT>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_linear_scan<IO, DX, DZ, OUT, UP>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, int(C::bytes));
         if (e != hipSuccess) return e;
     }
     const int64_t grid = int64_t(p.nwork) + (OUT ? p.tail * p.nroles : 0);
     if (grid == 0) return hipSuccess;
-    hipLaunchKernelGGL((k_linear_scan<IO, DX, DZ, OUT>), dim3(unsigned(grid)), dim3(C::T), C::bytes, s, p);
+    hipLaunchKernelGGL((k_linear_scan<IO, DX, DZ, OUT, UP>), dim3(unsigned(grid)), dim3(C::T), C::bytes, s, p);
     return hipGetLastError();
+}
+
+template <typename IO, int DX, int DZ, bool OUT>
+hipError_t launch_linear_inst(const LinParams &p, hipStream_t s) {
+    if constexpr (OUT && !std::is_same<IO, float>::value) {
+        bool fin = false;
+        for (int i = 0; i < p.nroles; ++i) fin |= p.role[i].fin != nullptr;
+        if (!fin) return launch_linear_planes<IO, DX, DZ, OUT, 2>(p, s);
+    }
+    return launch_linear_planes<IO, DX, DZ, OUT, 3>(p, s);
 }
 
 // The compiled tile of a size: 32, 64 or 128 channels.

@@ -10,35 +10,25 @@
 
 namespace m3 {
 
-// Joins the segment states of a cut sequence in place: slot s holds what the
-// segment before it left from zero and gets the state that segment s starts
-// from; the first slot gets the initial state.  Reading it here only lets the
-// scan's last segment write the final state over it.  blockIdx.x: (sequence,
-// head), blockIdx.y: 1024 entries of the state, blockIdx.z: scan.
+// Joins the segment states of a cut sequence in place: a slot holds what the
+// segment before it left from zero (the first one from the initial state) and
+// gets the state that its own segment starts from.  blockIdx.x: (sequence, head),
+// blockIdx.y: 1024 entries of the state, blockIdx.z: scan.
 __global__ __launch_bounds__(256) void k_linear_join(const LinParams p) {
     const LinRole &R = p.role[blockIdx.z];
     const int64_t b = blockIdx.x / p.H, h = blockIdx.x % p.H;
     const int64_t start = lin_start(p, b), next = lin_start(p, b + 1);
     const int64_t len = next > start ? next - start : 0, n = (len + (int64_t(1) << p.segbits) - 1) >> p.segbits;
-    if (!R.init && n <= 1) return;
-    const int64_t pool = lin_slot(p.slots, p.nstates, b);
-    if (pool < 0) return;
+    if (n <= 2) return;
+    if (lin_slot(p.slots, p.nstates, b) < 0) return;
     const int64_t area = int64_t(R.dx) * R.dz, e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
     if (e >= area) return;
-    floatx4 s{0.f, 0.f, 0.f, 0.f};
-    if (R.init) {
-        const int64_t at = (pool * p.H + h) * area + e;
-        float v[4];
-        if (R.init16) io<bf16>::load4(static_cast<const bf16 *>(R.init) + at, v);
-        else io<float>::load4(static_cast<const float *>(R.init) + at, v);
-        s = floatx4{v[0], v[1], v[2], v[3]};
-    }
     float *w = R.seg + (lin_first_slot(p, b) * p.H + h) * area + e;
     const int64_t step = p.H * area;
-    if (R.init) *reinterpret_cast<floatx4 *>(w) = s;
+    floatx4 s = *reinterpret_cast<const floatx4 *>(w + step);
     const LinDecay d(p.log_decay[h], double(int64_t(1) << p.segbits));
     constexpr int U = 8; // loads in flight
-    for (int64_t i = 1; i < n; i += U) {
+    for (int64_t i = 2; i < n; i += U) {
         floatx4 a[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -258,17 +248,23 @@ int64_t segment(const m3_linear_shape_t *s, int scans, int columns) {
     const int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
     const int64_t per = int64_t(heads(s)) * scans * columns;
     // two workgroups a compute unit, none much longer than the others: the
-    // chip is full without cutting
+    // chip is full without cutting (4 x 2048 x 64 x 64 backwards 122 us, 220 us cut)
     if (longest <= 256 || (s->batch * per >= 512 && longest * s->batch < 2 * s->tokens)) return 0;
-    int64_t L = 512;
-    while (L < 4096 && L * 2048 < s->tokens * per) L *= 2;
-    while (L > 256 && s->tokens * per < L * 512) L /= 2;
+    // else some 1024 workgroups, of at most 2048 tokens: fewer leave compute units
+    // to wait for the longest, more read and write states instead of rows
+    int64_t L = 256;
+    while (L < 2048 && L * 1024 < s->tokens * per) L *= 2;
     return longest > L ? L : 0;
+}
+int32_t few_segments(const m3_linear_shape_t *s, int64_t L) {
+    const int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
+    return L && longest <= 4 * L;
 }
 int64_t segment_slots(const m3_linear_shape_t *s, int64_t L) { return L ? s->tokens / L + s->batch : s->batch; }
 
 struct Layout {
     int64_t L, slots;
+    int32_t fold; // few segments: each reads the slots before its own instead of a pass that joins them
     size_t seg_f, seg_b, part[3], total; // byte offsets: segment states forwards, backwards, the parts of gradients
 };
 Layout prefill_layout(const m3_linear_shape_t *s) {
@@ -277,6 +273,7 @@ Layout prefill_layout(const m3_linear_shape_t *s) {
     const int zt = z_tile(s->value_dim, f32);
     w.L = segment(s, 1, (s->value_dim + zt - 1) / zt);
     w.slots = segment_slots(s, w.L);
+    w.fold = few_segments(s, w.L);
     if (w.L) w.total = round_up(size_t(w.slots) * heads(s) * s->key_dim * s->value_dim * 4);
     w.total = std::max(w.total, kAlign);
     return w;
@@ -286,6 +283,7 @@ Layout backward_layout(const m3_linear_shape_t *s) {
     const int32_t H = heads(s);
     w.L = segment(s, 3, 1);
     w.slots = segment_slots(s, w.L);
+    w.fold = few_segments(s, w.L);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -309,7 +307,15 @@ hipError_t launch_scan(LinParams p, bool f32, bool out, hipStream_t st) {
     const int dx = m3::lin_tile(p.role[0].dx), dz = z_tile(p.role[0].dz, f32);
     p.ztiles = (p.role[0].dz + dz - 1) / dz;
     for (int i = 1; i < p.nroles; ++i) p.ztiles = std::max(p.ztiles, (p.role[i].dz + dz - 1) / dz);
-    p.nwork = int32_t(p.nseg * p.H * p.ztiles * p.nroles);
+    // heads that share rows, and more neighbours of them where that leaves 32
+    // groups an XCD to spread: 65536 x 64 x 64 takes 681 us with 16 heads in a
+    // group, 740 us with one; 16 ragged sequences of 32 heads of 128 176 us with
+    // 16, 147 us with one
+    p.hg = 1;
+    for (int i = 0; i < p.nroles; ++i) p.hg = std::max(p.hg, std::max(p.role[i].xg, std::max(p.role[i].yg, p.role[i].zg)));
+    while (p.nroles == 1 && p.hg < 16 && p.H % (2 * p.hg) == 0 && p.nseg * (p.H / (2 * p.hg)) >= 8 * 32) p.hg *= 2;
+    p.group = p.hg * p.ztiles * p.nroles;
+    p.nwork = int32_t((p.nseg * (p.H / p.hg) + 7) / 8 * 8 * p.group);
     switch (dx) {
     case 32: return f32 ? m3::launch_linear_f32_32(p, dz, out, st) : m3::launch_linear_bf16_32(p, dz, out, st);
     case 64: return f32 ? m3::launch_linear_f32_64(p, dz, out, st) : m3::launch_linear_bf16_64(p, dz, out, st);
@@ -368,6 +374,7 @@ LinParams sequences(const m3_linear_shape_t *s, const int32_t *cu, const int32_t
     p.nstates = nstates;
     p.log_decay = ld;
     p.each = s->tokens / s->batch;
+    p.fold = w.fold;
     while (p.segbits < 30 && w.L >> p.segbits > 1) ++p.segbits;
     p.nseg = w.slots;
     return p;
@@ -441,7 +448,7 @@ m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q
     const bool f32 = shape->io_dtype == M3_DTYPE_F32;
     if (w.L) {
         if (launch_scans(p, 1, f32, false, stream) != hipSuccess) return M3_ERR_HIP;
-        if (launch_join(p, 1, stream) != hipSuccess) return M3_ERR_HIP;
+        if (!w.fold && launch_join(p, 1, stream) != hipSuccess) return M3_ERR_HIP;
     }
     return launch_scans(p, 1, f32, true, stream) == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
@@ -550,7 +557,7 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
         a.role[0].init16 = p.role[0].init16;
         a.role[1] = p.role[2];
         if (launch_scans(a, 2, f32, false, stream) != hipSuccess) return M3_ERR_HIP;
-        if (launch_join(a, 2, stream) != hipSuccess) return M3_ERR_HIP;
+        if (!w.fold && launch_join(a, 2, stream) != hipSuccess) return M3_ERR_HIP;
     }
     if (launch_scans(p, 3, f32, true, stream) != hipSuccess) return M3_ERR_HIP;
     if (sums.n && T > 0) {
