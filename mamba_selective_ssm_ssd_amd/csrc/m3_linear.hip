@@ -88,7 +88,10 @@ __global__ __launch_bounds__(256) void k_linear_sum(const LinSums p) {
 // Dk x Dv entries per sequence and head: bound by reading and writing it.  A
 // workgroup takes W columns of one state, four columns per lane in rows of
 // W / 4 lanes, and holds all its rows in registers: every load is issued before
-// the first is used.
+// the first is used.  States are read and written past the caches, as the layers
+// between two steps leave nothing of them there:
+// 100 us (5.4 TB/s) against 111 us with reads alone and 114 us with neither, over
+// 256 x 64 fp32 states of 64 x 64 taken in turn from more than the cache holds.
 // ---------------------------------------------------------------------------
 struct LinStepParams {
     const void *q, *k, *v;
@@ -101,14 +104,21 @@ struct LinStepParams {
     float scale;
 };
 
-// Four entries of a state.  An fp32 state is read past the cache, which the new
-// one then has for itself: 88 us against 101 us (6.1 and 5.3 TB/s) at 256 x 64
-// states of 64 x 64; a bf16 state gains nothing by it.
+typedef uint32_t u32x2_v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint4 step_load(const float *p) {
     const u32x4_v v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_v *>(p));
     return make_uint4(v.x, v.y, v.z, v.w);
 }
-__device__ __forceinline__ uint2 step_load(const bf16 *p) { return io4<bf16>::load(p); }
+__device__ __forceinline__ uint2 step_load(const bf16 *p) {
+    const u32x2_v v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_v *>(p));
+    return make_uint2(v.x, v.y);
+}
+__device__ __forceinline__ void step_store(float *p, const float v[4]) {
+    __builtin_nontemporal_store(floatx4{v[0], v[1], v[2], v[3]}, reinterpret_cast<floatx4 *>(p));
+}
+__device__ __forceinline__ void step_store(bf16 *p, const float v[4]) {
+    __builtin_nontemporal_store(u32x2_v{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])}, reinterpret_cast<u32x2_v *>(p));
+}
 
 template <typename IO, typename ST, int W>
 __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
@@ -124,9 +134,13 @@ __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
     IO *o = static_cast<IO *>(p.o) + b * p.ot + h * p.oh;
 
     int64_t slot = b;
+    int taken = 0;
     if (p.slots) {
         slot = p.slots[b];
         if (slot < 0 || slot >= p.nstates) return;
+        // an earlier sequence with the same slot has the state; looked for before
+        // the state's loads, which answer in order, are issued
+        for (int64_t j = tid; j < b; j += 256) taken |= p.slots[j] == int32_t(slot);
     }
     ST *st = static_cast<ST *>(p.state) + (slot * p.H + h) * p.dk * p.dv + c;
     typename io4<ST>::raw raw[NP];
@@ -145,7 +159,7 @@ __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
         }
     }
     if (in) io<IO>::load4(static_cast<const IO *>(p.v) + b * p.vt + (h / p.vg) * p.vh + c, v);
-    if (p.slots && lin_slot(p.slots, p.nstates, b) == kSlotTaken) {
+    if (p.slots && __syncthreads_or(taken)) {
         if (tid < L && in)
             for (int j = 0; j < 4; ++j) io<IO>::put(o + c + j, __builtin_nanf(""));
         return;
@@ -162,7 +176,7 @@ __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
                 s[j] = fmaf(kv[i], v[j], d(s[j]));
                 a[j] = fmaf(qv[i], s[j], a[j]);
             }
-            io<ST>::store4(st + (r0 + i * RP) * p.dv, s);
+            step_store(st + (r0 + i * RP) * p.dv, s);
         }
     // rows of one wave, then the four waves
 #pragma unroll

@@ -31,7 +31,8 @@ struct RotParams {
     float eps, inv_dim;
     const void *pos;
     const float *freq;
-    float *part;           // backward: [workgroup][2][dim] partial gradients of the weights
+    float *part;           // backward: [workgroup][dim] partial gradients of the weights
+    int32_t split;         // backward: workgroups of q, the others are k's
 };
 
 // The channels and angles of one lane.  HALVES: pairs (i, i + rot / 2), across
@@ -131,8 +132,10 @@ template <typename IO, int LPR, bool HALVES, int NR>
 __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
     constexpr int RPW = 64 / LPR;
     const int lane = threadIdx.x & 63, unit = lane % LPR, sub = lane / LPR;
-    const int items = p.r[0].items + p.r[1].items;
-    const int64_t item = int64_t(blockIdx.x) * (kRT / 64) + (threadIdx.x >> 6), token = item / items;
+    // counts of tokens and rows together stay below 2^31
+    const uint32_t items = p.r[0].items + p.r[1].items;
+    const uint32_t item = blockIdx.x * (kRT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t token = item / items;
     if (token >= p.tokens) return;
     int j = int(item % items);
     const bool is_q = j < p.r[0].items;
@@ -174,96 +177,94 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
 
 // With n = w r x, r = 1 / sqrt(mean x^2 + eps) and gn the gradient turned back:
 //     dw = sum gn r x,    dx = r w gn - (r^3 / dim) x sum(x w gn).
-// Workgroups walk the items with a fixed stride and keep their share of dw in
-// registers; k_norm_rotate_sum adds the shares in a fixed order.
+// Workgroups are q's or k's, walk their items with a fixed stride and keep their
+// share of dw in registers; k_norm_rotate_sum adds the shares in a fixed order.
 template <typename IO, int LPR, bool HALVES>
 __global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams p) {
     constexpr int RPW = 64 / LPR, NW = kRT / 64;
     __shared__ float part[NW][LPR * 8];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, unit = lane % LPR, sub = lane / LPR;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), unit = lane % LPR, sub = lane / LPR;
     RotLane<HALVES> l(p, unit);
-#pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind) {
-        const RotRows R = kind ? p.r[1] : p.r[0];
-        if (R.items == 0) continue;
-        float w[8], dw[8];
+    const bool is_q = int(blockIdx.x) < p.split;
+    const RotRows R = is_q ? p.r[0] : p.r[1];
+    const uint32_t first = is_q ? blockIdx.x : blockIdx.x - p.split, stride = is_q ? p.split : gridDim.x - p.split;
+    float w[8], dw[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = 1.f, dw[c] = 0.f;
-        if (R.w && l.in) {
-            io<float>::load4(R.w + l.c0, w);
-            io<float>::load4(R.w + l.c1, w + 4);
-        }
-        for (int64_t item = int64_t(blockIdx.x) * NW + wave; item < p.tokens * R.items; item += int64_t(gridDim.x) * NW) {
-            const int64_t token = item / R.items;
-            const int h0 = int(item % R.items) * kRows * RPW + sub;
-            const IO *x = static_cast<const IO *>(R.x) + token * R.xt;
-            const IO *g = static_cast<const IO *>(R.g) + token * R.gt;
-            IO *o = static_cast<IO *>(R.out) + token * R.ot;
-            RotRaw<IO, HALVES> rx[kRows], rg[kRows];
+    for (int c = 0; c < 8; ++c) w[c] = 1.f, dw[c] = 0.f;
+    if (R.w && l.in) {
+        io<float>::load4(R.w + l.c0, w);
+        io<float>::load4(R.w + l.c1, w + 4);
+    }
+    for (uint32_t item = first * NW + wave; item < uint32_t(p.tokens) * R.items; item += stride * NW) {
+        const int64_t token = item / uint32_t(R.items);
+        const int h0 = int(item % uint32_t(R.items)) * kRows * RPW + sub;
+        const IO *x = static_cast<const IO *>(R.x) + token * R.xt;
+        const IO *g = static_cast<const IO *>(R.g) + token * R.gt;
+        IO *o = static_cast<IO *>(R.out) + token * R.ot;
+        RotRaw<IO, HALVES> rx[kRows], rg[kRows];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i)
-                if (l.in && h0 + i * RPW < R.heads) {
-                    if (p.norm) rx[i].load(x + (h0 + i * RPW) * R.xh, l);
-                    rg[i].load(g + (h0 + i * RPW) * R.gh, l);
-                }
-            l.angles(p, unit, token);
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const bool on = l.in && h0 + i * RPW < R.heads;
-                float a[8] = {};
-                if (on) rg[i].unpack(a);
-                l.rotate(a, true);
-                if (p.norm) {
-                    float v[8] = {}, ss = 0.f, dot = 0.f;
-                    if (on) rx[i].unpack(v);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
-                    const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<LPR>(ss), p.inv_dim, p.eps));
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        dw[c] = fmaf(a[c] * r, v[c], dw[c]);
-                        a[c] *= w[c];
-                        dot = fmaf(v[c], a[c], dot);
-                    }
-                    const float m = row_sum<LPR>(dot) * p.inv_dim * (r * r);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) a[c] = r * (a[c] - m * v[c]);
-                }
-                if (on) rot_store(o + (h0 + i * RPW) * R.oh, l, a);
+        for (int i = 0; i < kRows; ++i)
+            if (l.in && h0 + i * RPW < R.heads) {
+                if (p.norm) rx[i].load(x + (h0 + i * RPW) * R.xh, l);
+                rg[i].load(g + (h0 + i * RPW) * R.gh, l);
             }
-        }
-        if (!R.w) continue;
+        l.angles(p, unit, token);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int i = 0; i < kRows; ++i) {
+            const bool on = l.in && h0 + i * RPW < R.heads;
+            float a[8] = {};
+            if (on) rg[i].unpack(a);
+            l.rotate(a, true);
+            if (p.norm) {
+                float v[8] = {}, ss = 0.f, dot = 0.f;
+                if (on) rx[i].unpack(v);
 #pragma unroll
-            for (int m = LPR; m < 64; m <<= 1) dw[c] += __shfl_xor(dw[c], m);
-        __syncthreads(); // the other kind's shares have been read
-        if (sub == 0)
+                for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
+                const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<LPR>(ss), p.inv_dim, p.eps));
 #pragma unroll
-            for (int c = 0; c < 8; ++c) part[wave][unit * 8 + c] = dw[c];
-        __syncthreads();
-        if (wave == 0 && sub == 0 && l.in) {
-            float *o = p.part + (int64_t(blockIdx.x) * 2 + kind) * p.dim;
+                for (int c = 0; c < 8; ++c) {
+                    dw[c] = fmaf(a[c] * r, v[c], dw[c]);
+                    a[c] *= w[c];
+                    dot = fmaf(v[c], a[c], dot);
+                }
+                const float m = row_sum<LPR>(dot) * p.inv_dim * (r * r);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                float s = 0.f;
-#pragma unroll
-                for (int v = 0; v < NW; ++v) s += part[v][unit * 8 + c];
-                o[c < 4 ? l.c0 + c : l.c1 + c - 4] = s;
+                for (int c = 0; c < 8; ++c) a[c] = r * (a[c] - m * v[c]);
             }
+            if (on) rot_store(o + (h0 + i * RPW) * R.oh, l, a);
+        }
+    }
+    if (!R.w) return;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int m = LPR; m < 64; m <<= 1) dw[c] += __shfl_xor(dw[c], m);
+    if (sub == 0)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) part[wave][unit * 8 + c] = dw[c];
+    __syncthreads();
+    if (wave == 0 && sub == 0 && l.in) {
+        float *o = p.part + int64_t(blockIdx.x) * p.dim;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < NW; ++v) s += part[v][unit * 8 + c];
+            o[c < 4 ? l.c0 + c : l.c1 + c - 4] = s;
         }
     }
 }
 
 // Sum of the workgroups' shares, four channels of one weight per workgroup: a
 // share to a thread, then the threads of a wave and the waves in pairs.
-__global__ __launch_bounds__(1024) void k_norm_rotate_sum(const float *part, int n, int dim, float *dq, float *dk) {
+__global__ __launch_bounds__(1024) void k_norm_rotate_sum(const float *part, int split, int n, int dim, float *dq, float *dk) {
     __shared__ floatx4 s[16];
-    const int c = blockIdx.x * 4, kind = blockIdx.y;
-    float *out = kind ? dk : dq;
+    const int c = blockIdx.x * 4;
+    float *out = blockIdx.y ? dk : dq;
     if (!out) return;
     floatx4 a{0.f, 0.f, 0.f, 0.f};
-    for (int i = threadIdx.x; i < n; i += 1024) a += *reinterpret_cast<const floatx4 *>(part + (int64_t(i) * 2 + kind) * dim + c);
+    for (int i = (blockIdx.y ? split : 0) + threadIdx.x; i < (blockIdx.y ? n : split); i += 1024)
+        a += *reinterpret_cast<const floatx4 *>(part + int64_t(i) * dim + c);
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1)
 #pragma unroll
@@ -354,14 +355,19 @@ int32_t items(const m3_rotary_shape_t *s, int32_t heads) {
     return (heads + set - 1) / set;
 }
 
-// Workgroups of the gradients: at most the four per compute unit that are
-// resident at once (128 registers), so that they share the rows evenly and leave
-// few partial sums.  Twice as many took as long (76 us at 8192 x 128 x 64) and
-// their sum 1 us more.
-constexpr int64_t kBackGrid = 1024;
-int64_t backward_grid(const m3_rotary_shape_t *s) {
-    const int64_t n = s->tokens * std::max(items(s, s->q_heads), items(s, s->k_heads));
-    return std::max<int64_t>(1, std::min<int64_t>((n + 3) / 4, kBackGrid));
+// Workgroups of the gradients, for q and for k, in the ratio of their items: at
+// most the four per compute unit that are resident at once (128 registers), so
+// that they share the rows evenly and leave few partial sums.  Twice as many took
+// as long (76 us at 8192 x 128 x 64) and their sum 1 us more.
+struct BackGrid {
+    int64_t q, k;
+};
+BackGrid backward_grid(const m3_rotary_shape_t *s) {
+    const int64_t iq = items(s, s->q_heads), ik = items(s, s->k_heads), n = (s->tokens * (iq + ik) + 3) / 4;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(n, 1024));
+    if (ik == 0) return {grid, 0};
+    const int64_t k = std::max<int64_t>(1, grid * ik / (iq + ik));
+    return {std::max<int64_t>(1, grid - k), k};
 }
 
 m3::RotParams params(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_rows_t *k, const void *pos,
@@ -425,7 +431,8 @@ m3_status_t m3_norm_rotate(const m3_rotary_shape_t *shape, const m3_rows_t *q, c
 
 size_t m3_norm_rotate_backward_workspace_bytes(const m3_rotary_shape_t *shape) {
     if (check_shape(shape) != M3_OK) return 0;
-    return size_t(backward_grid(shape)) * 2 * shape->dim * sizeof(float);
+    const BackGrid g = backward_grid(shape);
+    return size_t(g.q + g.k) * shape->dim * sizeof(float);
 }
 
 m3_status_t m3_norm_rotate_backward(const m3_rotary_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
@@ -450,13 +457,15 @@ m3_status_t m3_norm_rotate_backward(const m3_rotary_shape_t *shape, const m3_row
     p.r[0].g = gq->data; p.r[0].gt = gq->token_stride; p.r[0].gh = gq->head_stride;
     if (shape->k_heads) { p.r[1].g = gk->data; p.r[1].gt = gk->token_stride; p.r[1].gh = gk->head_stride; }
     p.part = static_cast<float *>(workspace);
-    const int64_t grid = backward_grid(shape);
+    const BackGrid g = backward_grid(shape);
+    const int64_t grid = g.q + g.k;
+    p.split = int32_t(g.q);
     const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, shape->halves, grid, true, stream)
                                                          : m3::launch_rotary_io<m3::bf16>(p, shape->halves, grid, true, stream);
     if (e != hipSuccess) return M3_ERR_HIP;
     if (dq_weight || dk_weight) {
         hipLaunchKernelGGL(m3::k_norm_rotate_sum, dim3(unsigned(shape->dim / 4), 2), dim3(1024), 0, stream,
-                           p.part, int(grid), shape->dim, dq_weight, dk_weight);
+                           p.part, p.split, int(grid), shape->dim, dq_weight, dk_weight);
         if (hipGetLastError() != hipSuccess) return M3_ERR_HIP;
     }
     return M3_OK;
