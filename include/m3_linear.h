@@ -41,8 +41,8 @@
  * everything before the token itself).  The weights of a chunk are taken in
  * fp32 from it, and no gradient is formed for it.  A non-finite value of one
  * token reaches, within its sequence and head, the outputs of its own chunk
- * (64 tokens; 32 with fp32 I/O; counted from the end of the sequence for the
- * gradients of k and v) and of everything behind it, and no other sequence.
+ * (at most 64 tokens; counted from the end of the sequence for the gradients
+ * of k and v) and of everything behind it, and no other sequence.
  *
  * Ownership, streams, threads and errors are those of m3_ssm.h: the caller
  * owns every buffer and the workspace, calls only enqueue kernels, nothing is
@@ -69,7 +69,9 @@ typedef struct {
 /* Supported: key_dim and value_dim multiples of 8 from 8 to 128; any head
  * counts that divide the largest; batch >= 1; tokens >= 0 (decode: ignored,
  * there is one token per sequence).  M3_ERR_INVALID_ARGUMENT for counts that
- * do not divide, M3_ERR_UNSUPPORTED for other sizes. */
+ * do not divide, M3_ERR_UNSUPPORTED for other sizes, and for more sequences,
+ * tokens and heads than one launch has threads for: (batch + 8 + tokens / 1024)
+ * H up to 2795690, for a decode step (batch + 8) H up to 8388095. */
 typedef struct {
     int64_t batch;      /* sequences                                              */
     int64_t tokens;     /* rows of q, k, v and o                                  */

@@ -28,7 +28,10 @@ extern "C" {
 
 /* Supported: dim a multiple of 8 from 8 to 256; rot a multiple of 8 from 8 to
  * dim; axes 1 to 4; tokens >= 0; q_heads >= 1, k_heads >= 0 (0: no keys, their
- * pointers are not read).  Other sizes are M3_ERR_UNSUPPORTED. */
+ * pointers are not read).  Other sizes are M3_ERR_UNSUPPORTED, and so are more
+ * rows than one launch has threads for: tokens (ceil(q_heads / n) +
+ * ceil(k_heads / n)) up to 2^26 - 5, with 256 / n the power of two that dim / 8
+ * lanes fit in. */
 typedef struct {
     int64_t tokens;
     int32_t q_heads, k_heads;

@@ -163,17 +163,18 @@ __device__ __forceinline__ void lunsplit(const lfrag<PL> &f, float a[8]) {
 
 // ---------------------------------------------------------------------------
 // Tile of one scan.  Q rows per chunk, DX x DZ state columns of a workgroup of
-// four or eight waves; z columns beyond DZ are another workgroup's.
+// four waves; z columns beyond DZ are another workgroup's.
 // ---------------------------------------------------------------------------
 template <typename IO, int DX, int DZ, bool OUT>
 struct LinCfg {
     static constexpr bool F32 = std::is_same<IO, float>::value;
     static constexpr int PL = F32 ? 3 : 1;
-    static constexpr int Q = F32 || (OUT && DX == 128 && DZ == 128) ? 32 : 64;
+    static constexpr int Q = F32 || (OUT && DX == 128 && DZ == 128) ? 32 : 64; // 64 rows of 128 x 128 spill (442 us for 219)
     static constexpr int MP = DX / 32, NP = DZ / 32; // 32 x 32 blocks of the state, 16 x 16 tiles in pairs
     // the state's tiles over the waves: MW along x (MTW tiles each, a pair of
     // one block where it is two), NW along z
-    static constexpr int W = !F32 && !OUT && DX == 128 && DZ == 128 ? 8 : 4, T = 64 * W;
+    static constexpr int W = 4, T = 64 * W;
+    static constexpr int WAVES = OUT || DX * DZ > 64 * 128 ? 2 : DX * DZ > 64 * 64 ? 3 : 4; // a SIMD, as far as registers go round
     static constexpr int MW = 2 * MP < W ? 2 * MP : W, MTW = 2 * MP / MW, NW = W / MW, NTW = 2 * NP / NW;
     static_assert(MTW <= 2 && NTW >= 1, "tiles of a wave");
     // the output's 16-row tiles over the waves: RW along the rows, OW along z (NOT tiles each)
@@ -247,11 +248,8 @@ struct LinBuf {
         const u32x4_v v = __builtin_bit_cast(u32x4_v, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
         return make_uint4(v.x, v.y, v.z, v.w);
     }
-    // past: written past the caches (non-temporal)
-    __device__ __forceinline__ void store(uint32_t at, uint4 v, bool past) const {
-        const u32x4_v q{v.x, v.y, v.z, v.w};
-        if (past) __builtin_amdgcn_raw_buffer_store_b128(q, r, at, 0, 2);
-        else __builtin_amdgcn_raw_buffer_store_b128(q, r, at, 0, 0);
+    __device__ __forceinline__ void store(uint32_t at, uint4 v) const {
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4_v{v.x, v.y, v.z, v.w}, r, at, 0, 0);
     }
     __device__ __forceinline__ float get(uint32_t at) const { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0)); }
     __device__ __forceinline__ float get16(uint32_t at) const { return bits_to_f32(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0))); }
@@ -370,9 +368,15 @@ __device__ __forceinline__ void lin_tail(const LinParams &p, const LinRole &R, i
     if (R.out32) return;
     const int64_t lo = lin_start(p, 0), hi = lin_start(p, p.batch);
     const int64_t n = lo + (p.tokens > hi ? p.tokens - hi : 0);
+    const int u = R.dz / 8, units = p.H * u;
+    const float zero[4] = {};
     for (int64_t i = wg; i < n; i += p.tail) {
         IO *o = static_cast<IO *>(R.out) + (i < lo ? i : hi + (i - lo)) * R.ot;
-        for (int e = threadIdx.x; e < p.H * R.dz; e += blockDim.x) io<IO>::put(o + (e / R.dz) * R.oh + e % R.dz, 0.f);
+        for (int e = threadIdx.x; e < units; e += blockDim.x) {
+            IO *c = o + (e / u) * R.oh + e % u * 8;
+            io<IO>::store4(c, zero);
+            io<IO>::store4(c + 4, zero);
+        }
     }
 }
 
@@ -387,7 +391,7 @@ __device__ __forceinline__ const LinParams &lin_args() {
 // the weighted y that join the state; three keep it to fp32 accuracy, two (2^-17)
 // do where it is only rounded to bf16 and not handed out.
 template <typename IO, int DX, int DZ, bool OUT, int UP>
-__global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k_linear_scan(const LinParams p) {
+__global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, OUT>::WAVES)) void k_linear_scan(const LinParams p) {
     typedef LinCfg<IO, DX, DZ, OUT> C;
     constexpr int PL = C::PL, Q = C::Q, KS = C::KS;
     extern __shared__ __align__(16) uint16_t lds[];
@@ -452,21 +456,17 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k
     if (OUT) xr.init(R.x, t0, R.xt, (h / R.xg) * R.xh, R.dx, R.rev);
     yr.init(R.y, t0, R.yt, (h / R.yg) * R.yh, R.dx, R.rev);
     zr.init(R.z, t0, R.zt, (h / R.zg) * R.zh + z0, R.dz - z0, R.rev);
-    // rows on their way: a chunk's, or two chunks' where there is little else to do
-    constexpr int AHEAD = 1;
-    LinRegs<IO, Q, DX, C::T> xq[1], yq[AHEAD];
-    LinRegs<IO, Q, DZ, C::T> zq[AHEAD];
-    int left = int(pos1 - pos), ahead = left; // rows to go, and to load
-    auto load = [&](int set) __attribute__((always_inline)) {
-        if (ahead <= 0) return;
-        const int rows = ahead < Q ? ahead : Q;
-        if (OUT) xr.load(xq[0], rows);
-        yr.load(yq[set], rows);
-        zr.load(zq[set], rows);
-        ahead -= rows;
+    LinRegs<IO, Q, DX, C::T> xq, yq; // the next chunk's rows, on their way
+    LinRegs<IO, Q, DZ, C::T> zq;
+    int left = int(pos1 - pos); // rows to go
+    auto load = [&]() __attribute__((always_inline)) {
+        if (left <= 0) return;
+        const int rows = left < Q ? left : Q;
+        if (OUT) xr.load(xq, rows);
+        yr.load(yq, rows);
+        zr.load(zq, rows);
     };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) load(i);
+    load();
 
     const int es = R.rev ? 0 : 1;
     const float ld2 = ld * 1.44269504f;
@@ -552,12 +552,10 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k
     const int osize = C::F32 || R.out32 ? 4 : 2;
     const uint32_t ostep = uint32_t(R.ot) * osize;
     const uint32_t oat = uint32_t(R.rev ? Q - 1 - (16 * rt + r16) : 16 * rt + r16) * ostep + (osize == 4 ? 16 * g : 32 * (g & 1) + 16 * (g >> 1));
-    // several scans of a launch share their rows: what they write leaves the cache
-    // to those, but for the parts that are read again next
-    const bool rev = R.rev, past = p.nroles > 1 && !R.out32;
+    const bool rev = R.rev;
     out += (t0 * R.ot + h * R.oh + z0) * osize;
 
-    auto chunk = [&](int set) __attribute__((always_inline)) {
+    while (left > 0) {
         const int rows = left < Q ? left : Q;
         left -= rows;
         float decay;
@@ -568,9 +566,9 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k
             const int i = 16 * rt + r16 - (Q - rows);
             from_start = i >= 0 ? R.a_init * lin_power(ld2, i + es) : 0.f;
         }
-        if (OUT) xq[0].template stage<C::XP>(xs);
-        yq[set].template stage<C::XP>(ys);
-        zq[set].template stage<C::ZP>(zs);
+        if (OUT) xq.template stage<C::XP>(xs);
+        yq.template stage<C::XP>(ys);
+        zq.template stage<C::ZP>(zs);
         if (OUT) {
 #pragma unroll
             for (int j = 0; j < C::NTW; ++j) {
@@ -590,7 +588,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k
             }
         }
         __syncthreads();
-        load(set);
+        load();
 
         floatx4 O[C::NOT]; // out^T, tile j: channel z0 + 16 tile(j) + 4 g + v of row 16 rt + r16
         lfrag<PL> pf[KS];  // weights of the chunk's rows in row 16 rt + r16
@@ -692,7 +690,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k
             if (osize == 4) {
 #pragma unroll
                 for (int j = 0; j < C::NOT; ++j)
-                    o.store(16 * tile(j) + 4 * g < dz ? at + 64 * tile(j) : kNowhere, __builtin_bit_cast(uint4, O[j]), past);
+                    o.store(16 * tile(j) + 4 * g < dz ? at + 64 * tile(j) : kNowhere, __builtin_bit_cast(uint4, O[j]));
             } else if constexpr (!C::F32) {
                 // lanes of neighbouring groups swap halves of two tiles: eight
                 // neighbouring channels each
@@ -706,15 +704,11 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (OUT ? 2 : 4)) void k
                     const int n = tile(j) & ~1;
                     const auto a = __builtin_amdgcn_permlane16_swap(pack2_bf16(O[j][0], O[j][1]), pack2_bf16(O[j + 1][0], O[j + 1][1]), false, false);
                     const auto b = __builtin_amdgcn_permlane16_swap(pack2_bf16(O[j][2], O[j][3]), pack2_bf16(O[j + 1][2], O[j + 1][3]), false, false);
-                    o.store(16 * n + 16 * (g & 1) + 8 * (g >> 1) < dz ? at + 32 * n : kNowhere, make_uint4(a[0], b[0], a[1], b[1]), past);
+                    o.store(16 * n + 16 * (g & 1) + 8 * (g >> 1) < dz ? at + 32 * n : kNowhere, make_uint4(a[0], b[0], a[1], b[1]));
                 }
             }
         }
         __syncthreads();
-    };
-    while (left > 0) {
-        chunk(0);
-        if (AHEAD == 2 && left > 0) chunk(1);
     }
 
     if (OUT && (!last || !R.fin)) return;
@@ -744,6 +738,7 @@ hipError_t launch_linear_planes(const LinParams &p, hipStream_t s) {
 
 template <typename IO, int DX, int DZ, bool OUT>
 hipError_t launch_linear_inst(const LinParams &p, hipStream_t s) {
+    // gradients of 4 x 2048 x 64 x 64: 168 us with two planes, 174 with three
     if constexpr (OUT && !std::is_same<IO, float>::value) {
         bool fin = false;
         for (int i = 0; i < p.nroles; ++i) fin |= p.role[i].fin != nullptr;

@@ -196,7 +196,9 @@ __global__ __launch_bounds__(256) void k_linear_step(const LinStepParams p) {
 
 template <typename IO, typename ST>
 hipError_t launch_linear_step(LinStepParams &p, hipStream_t s) {
-    const bool wide = p.batch * p.H * ((p.dv + 63) / 64) >= 1024;
+    // below two workgroups a compute unit, twice as many of half the columns: 32
+    // states of 128 x 128 4.7 us (5.2 with 64 columns); 512 of 64 x 64 6.0 us (6.7 with 32)
+    const bool wide = p.batch * p.H * ((p.dv + 63) / 64) >= 512;
     p.slices = wide ? (p.dv + 63) / 64 : (p.dv + 31) / 32;
     const dim3 grid(unsigned(p.batch * p.H * p.slices));
     if (wide) hipLaunchKernelGGL((k_linear_step<IO, ST, 64>), grid, dim3(256), 0, s, p);
@@ -230,7 +232,11 @@ m3_status_t check_shape(const m3_linear_shape_t *s, bool decode) {
     // counts of sequences and tokens are indexed in 32 bits (cu_seqlens, slots), workgroups too
     if (s->batch > (int64_t(1) << 31) - 2 || H > (1 << 20)) return M3_ERR_UNSUPPORTED;
     if (!decode && s->tokens > (int64_t(1) << 31) - 1) return M3_ERR_UNSUPPORTED;
-    if (double(s->batch) * H * 6 * (decode ? 1 : 1 + double(s->tokens) / s->batch / 256) > 2147483647.0) return M3_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads: workgroups of 256 for each head, two column
+    // tiles and three scans of a segment slot: one per sequence, and one per 1024 tokens
+    // but where these are 512 at most
+    const double slots = (double(s->batch) + 8 + (decode ? 0. : double(s->tokens) / 1024)) * H + 512;
+    if (slots * 256 * (decode ? 2 : 6) > 4294967295.0) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
 
@@ -261,15 +267,22 @@ int z_tile(int dz, bool f32) { return f32 ? std::min(m3::lin_tile(dz), 64) : m3:
 int64_t segment(const m3_linear_shape_t *s, int scans, int columns) {
     const int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
     const int64_t per = int64_t(heads(s)) * scans * columns;
-    // two workgroups a compute unit, none much longer than the others: the
-    // chip is full without cutting (4 x 2048 x 64 x 64 backwards 122 us, 220 us cut)
-    if (longest <= 256 || (s->batch * per >= 512 && longest * s->batch < 2 * s->tokens)) return 0;
-    // else some 1024 workgroups, of at most 2048 tokens: fewer leave compute units
-    // to wait for the longest, more read and write states instead of rows
+    // Enough workgroups for most compute units, none much longer than the others:
+    // the chip is full without cutting, and nothing is read twice (8 x 2048 x 32 x
+    // 128 144 us, 177 cut by 1024; gradients of 4 x 2048 x 32 x 128 184 us, 222 cut).
+    if (longest <= 256 || (s->batch * per >= 192 && longest * s->batch < 2 * s->tokens)) return 0;
+    // Else two workgroups a compute unit, all that fit at once: longer segments leave
+    // some idle, shorter ones read and write states instead of rows (16 ragged
+    // sequences of 1024 x 32 x 128: 207 us with segments of 1024, 227 of 512, 240 of
+    // 2048).  The gradients' scans differ more: four (4096 x 32 x 128 135 us, 148 with
+    // two).  1024 tokens at most: 65536 x 64 x 64 703 us, 729 with 2048.
     int64_t L = 256;
-    while (L < 2048 && L * 1024 < s->tokens * per) L *= 2;
+    while (L < 1024 && L * (scans > 1 ? 1024 : 512) < s->tokens * per) L *= 2;
     return longest > L ? L : 0;
 }
+// With four segments or fewer each folds the states before its own instead of a
+// pass that joins them: 1000 x 32 x 128 36 us, 38 joined; gradients of 8192 x 32 x
+// 128 242 us, 247 joined, but 292 where eight are folded.
 int32_t few_segments(const m3_linear_shape_t *s, int64_t L) {
     const int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
     return L && longest <= 4 * L;
@@ -520,7 +533,7 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
     unsigned char *ws = static_cast<unsigned char *>(workspace);
 
     LinParams p = sequences(shape, cu_seqlens, nullptr, shape->batch, log_decay, w);
-    p.tail = cu_seqlens ? 16 : 0;
+    p.tail = cu_seqlens ? 64 : 0;
     const Rows rq{q, shape->q_heads, shape->key_dim}, rk{k, shape->k_heads, shape->key_dim}, rv{v, shape->v_heads, shape->value_dim}, rg{go, H, dv};
     const Rows x[3] = {rg, rv, rk}, y[3] = {rv, rg, rq}, z[3] = {rk, rq, rg};
     const m3_rows_t *out[3] = {gq, gk, gv};
@@ -576,7 +589,8 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
     if (launch_scans(p, 3, f32, true, stream) != hipSuccess) return M3_ERR_HIP;
     if (sums.n && T > 0) {
         sums.seq = p;
-        const dim3 grid(2048, unsigned(sums.n));
+        const int64_t n = T * H * (std::max(dk, dv) / 8); // no row has more heads than H
+        const dim3 grid(unsigned(std::min<int64_t>(2048, (n + 255) / 256)), unsigned(sums.n));
         if (f32) hipLaunchKernelGGL(m3::k_linear_sum<float>, grid, dim3(256), 0, stream, sums);
         else hipLaunchKernelGGL(m3::k_linear_sum<m3::bf16>, grid, dim3(256), 0, stream, sums);
         if (hipGetLastError() != hipSuccess) return M3_ERR_HIP;

@@ -15,7 +15,7 @@
 namespace m3 {
 
 constexpr int kRT = 256;   // threads, four waves
-constexpr int kRows = 4;   // row sets per wave and token (twice as many where there are waves enough)
+constexpr int kRows = 4;   // row sets per wave and token at most
 
 struct RotRows {
     const void *x, *g;     // input rows; upstream gradient (backward)
@@ -159,6 +159,7 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
     l.angles(p, unit, token);
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
+        if (i && j * NR * RPW + i * RPW >= R.heads) break; // the same for the whole wave
         const bool on = l.in && h0 + i * RPW < R.heads;
         float v[8] = {};
         if (on) raw[i].unpack(v);
@@ -211,6 +212,7 @@ __global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams
         l.angles(p, unit, token);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
+            if (i && h0 - sub + i * RPW >= R.heads) break; // the same for the whole wave
             const bool on = l.in && h0 + i * RPW < R.heads;
             float a[8] = {};
             if (on) rg[i].unpack(a);
@@ -292,13 +294,17 @@ hipError_t launch_rotary(RotParams &p, int64_t grid, bool back, hipStream_t s) {
         hipLaunchKernelGGL((k_norm_rotate_backward<IO, LPR, HALVES>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
         return hipGetLastError();
     }
-    // twice the rows for a wave's angles where that still leaves eight waves a SIMD
-    const bool two = grid >= 2 * 2048;
-    if (two)
-        for (RotRows &r : p.r) r.items = (r.heads + 2 * kRows * (64 / LPR) - 1) / (2 * kRows * (64 / LPR));
-    const int64_t n = (p.tokens * (p.r[0].items + p.r[1].items) + 3) / 4;
-    if (two) hipLaunchKernelGGL((k_norm_rotate<IO, LPR, HALVES, 2 * kRows>), dim3(unsigned(n)), dim3(kRT), 0, s, p);
-    else hipLaunchKernelGGL((k_norm_rotate<IO, LPR, HALVES, kRows>), dim3(unsigned(n)), dim3(kRT), 0, s, p);
+    // Below two waves a SIMD, or where a set holds all heads, a wave takes one set:
+    // 512 x 40 x 128 4.8 us (5.4 with up to four sets), 32768 x 10 x 64 33 us (37).
+    // Else its angles serve up to four: 16384 x 40 x 128 57 us (5.9 TB/s; 79 with
+    // one, 60 with six), 1024 x 40 x 128 7.5 us (8.5 with one).
+    if (grid < 512 || std::max(p.r[0].heads, p.r[1].heads) <= 64 / LPR) {
+        for (RotRows &r : p.r) r.items = (r.heads + 64 / LPR - 1) / (64 / LPR);
+        grid = (p.tokens * (p.r[0].items + p.r[1].items) + 3) / 4;
+        hipLaunchKernelGGL((k_norm_rotate<IO, LPR, HALVES, 1>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
+    } else {
+        hipLaunchKernelGGL((k_norm_rotate<IO, LPR, HALVES, kRows>), dim3(unsigned(grid)), dim3(kRT), 0, s, p);
+    }
     return hipGetLastError();
 }
 
@@ -325,6 +331,12 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Items of one token: groups of kRows row sets.
+int32_t items(const m3_rotary_shape_t *s, int32_t heads) {
+    const int set = m3::kRows * (64 / m3::rot_lanes(s->dim));
+    return (heads + set - 1) / set;
+}
+
 m3_status_t check_shape(const m3_rotary_shape_t *s) {
     if (!s) return M3_ERR_INVALID_ARGUMENT;
     if (s->io_dtype != M3_DTYPE_F32 && s->io_dtype != M3_DTYPE_BF16) return M3_ERR_INVALID_ARGUMENT;
@@ -333,7 +345,10 @@ m3_status_t check_shape(const m3_rotary_shape_t *s) {
     if (s->norm && !(s->eps >= 0.f)) return M3_ERR_INVALID_ARGUMENT;
     if (s->dim % 8 || s->dim > 256 || s->rot % 8 || s->axes > 4) return M3_ERR_UNSUPPORTED;
     if (s->q_heads > (1 << 20) || s->k_heads > (1 << 20)) return M3_ERR_UNSUPPORTED;
+    // rows are counted in 32 bits, and a launch has fewer than 2^32 threads: a wave of 64
+    // for 64 / lanes rows or fewer
     if (double(s->tokens) * (double(s->q_heads) + s->k_heads + 2) > 2147483647.0) return M3_ERR_UNSUPPORTED;
+    if ((double(s->tokens) * (items(s, s->q_heads) + items(s, s->k_heads)) + 4) * 64 > 4294967295.0) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
 
@@ -348,11 +363,6 @@ bool rows_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim, boo
     const bool by_token = (tokens == 1 || t >= (heads - 1) * h + dim) && (heads == 1 || h >= dim);
     const bool by_head = (heads == 1 || h >= (tokens - 1) * t + dim) && (tokens == 1 || t >= dim);
     return by_token || by_head;
-}
-
-int32_t items(const m3_rotary_shape_t *s, int32_t heads) {
-    const int set = m3::kRows * (64 / m3::rot_lanes(s->dim));
-    return (heads + set - 1) / set;
 }
 
 // Workgroups of the gradients, for q and for k, in the ratio of their items: at

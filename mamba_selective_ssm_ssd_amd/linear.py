@@ -8,8 +8,8 @@ q [T,Hq,Dk], k [T,Hk,Dk], v [T,Hv,Dv] in float32 or bfloat16; each head count
 divides H = max(Hq,Hk,Hv), and head h reads row h // (H // Hq) of q (k and v
 likewise).  log_decay [H] float32.  Dk and Dv are multiples of 8 up to 128.
 Channels of a row must be contiguous and rows 16-byte aligned; the token and
-head axes may have any stride that is a multiple of 8 elements, so slices of
-one projection's output need no copy.
+head axes may have any stride that is a multiple of 8 elements, the tokens' at
+least a row's channels, so slices of one projection's output need no copy.
 
 Sequences are packed along T: ``cu_seqlens`` [B+1] int32 on the device gives
 sequence b the tokens cu_seqlens[b]:cu_seqlens[b+1] (empty ones included).
@@ -30,7 +30,7 @@ from __future__ import annotations
 import torch
 
 from . import capi
-from .mixer import _IO, _ptr
+from .mixer import _IO
 
 
 # A step of a few rows is over in the time that its wrapper takes, so the checks
@@ -45,11 +45,6 @@ def _device(t: torch.Tensor) -> int:
     if device < 0 or device != torch.cuda.current_device():
         raise ValueError(f"tensors must be on the current device, got {t.device}")
     return device
-
-
-def _on(t: torch.Tensor, name: str, device: int) -> None:
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
 def _rows(t: torch.Tensor, name: str, dtype, device: int):
@@ -76,37 +71,25 @@ def _rows(t: torch.Tensor, name: str, dtype, device: int):
     return capi.m3_rows_t(t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0), (b, n, h, d)
 
 
-def _new_rows(shape, like: torch.Tensor):
-    """A new contiguous tensor of rows, and its rows."""
-    t = torch.empty(shape, device=like.device, dtype=like.dtype)
-    h, d = shape[-2:]
-    return t, capi.m3_rows_t(t.data_ptr(), h * d, d)
+def _like_rows(t: torch.Tensor, heads: int, channels: int):
+    """A new contiguous tensor of the shape and type of rows ``t``, and its rows."""
+    new = torch.empty_like(t, memory_format=torch.contiguous_format)
+    return new, capi.m3_rows_t(new.data_ptr(), heads * channels, channels)
 
 
-def _index(t, name: str, n: int | None, device: int) -> int | None:
+def _ptr(t, name: str, shape: tuple | None, dtype, device: int) -> int | None:
+    """Address of a contiguous tensor of that shape and type (None for None)."""
     if t is None:
         return None
-    _on(t, name, device)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    return _ptr(t, name, torch.int32)
-
-
-def _pool(t, name: str, shape: tuple, device: int, dtype) -> int | None:
-    """Address of a state pool [n,H,Dk,Dv]."""
-    if t is None:
-        return None
-    _on(t, name, device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    return _ptr(t, name, dtype)
-
-
-def _decay(t, H, device: int) -> int:
-    _on(t, "log_decay", device)
-    if t.shape != (H,):
-        raise ValueError(f"log_decay must be [{H}], got {tuple(t.shape)}")
-    return _ptr(t, "log_decay", torch.float32)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _operands(q, k, v):
@@ -135,21 +118,21 @@ def _sequences(b, T, cu_seqlens, device: int):
         return (1, None, T) if b is None else (b, None, T // b if b else 0)
     if b is not None and b != 1:
         raise ValueError("cu_seqlens needs rows packed along one axis")
-    cu = _index(cu_seqlens, "cu_seqlens", None, device)
-    n = cu_seqlens.shape[0]
-    if n < 2:
-        raise ValueError("cu_seqlens must have at least two entries")
-    return n - 1, cu, T
+    cu = _ptr(cu_seqlens, "cu_seqlens", None, torch.int32, device)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError(f"cu_seqlens must be [B+1] with two entries or more, got {tuple(cu_seqlens.shape)}")
+    return cu_seqlens.shape[0] - 1, cu, T
 
 
-def _workspace(workspace, need: int, device: int, where: str):
+def _workspace(workspace, need: int, like: torch.Tensor, device: int, where: str):
     """(address, bytes, owner) of the given workspace or a new one."""
     if workspace is None:
         if need == 0:
             raise capi.M3Error(capi.M3_ERR_UNSUPPORTED, where)
-        workspace = torch.empty((need,), device=f"cuda:{device}", dtype=torch.uint8)
+        workspace = like.new_empty((need,), dtype=torch.uint8)
         return workspace.data_ptr(), need, workspace
-    _on(workspace, "workspace", device)
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -195,16 +178,18 @@ def prefill(q, k, v, log_decay, state=None, final=None, want_final=True, *, cu_s
                                    dk ** -0.5 if scale is None else scale)
     out_shape = (T, H, dv) if b is None else (b, T // b if b else 0, H, dv)
     if o is None:
-        o, ro = _new_rows(out_shape, q)
+        o = q.new_empty(out_shape)
+        ro = capi.m3_rows_t(o.data_ptr(), H * dv, dv)
     elif o.shape != out_shape:
         raise ValueError(f"o must be {out_shape}, got {tuple(o.shape)}")
     else:
         ro, _ = _rows(o, "o", io, dev)
-    wp, wn, workspace = _workspace(workspace, capi.m3_linear_prefill_workspace_bytes(shape), dev, "m3_linear_prefill")
+    wp, wn, workspace = _workspace(workspace, capi.m3_linear_prefill_workspace_bytes(shape), q, dev,
+                                   "m3_linear_prefill")
     pool = (n, H, dk, dv)
-    rc = capi.m3_linear_prefill(shape, rq, rk, rv, _decay(log_decay, H, dev), cu, _index(slots, "slots", batch, dev),
-                                n, _pool(state, "state", pool, dev, sd), _pool(final, "final", pool, dev, sd),
-                                ro, wp, wn, _stream(dev))
+    rc = capi.m3_linear_prefill(shape, rq, rk, rv, _ptr(log_decay, "log_decay", (H,), torch.float32, dev), cu,
+                                _ptr(slots, "slots", (batch,), torch.int32, dev), n, _ptr(state, "state", pool, sd, dev),
+                                _ptr(final, "final", pool, sd, dev), ro, wp, wn, _stream(dev))
     if rc:
         raise capi.M3Error(rc, "m3_linear_prefill")
     return o, final
@@ -224,15 +209,17 @@ def decode_step(q, k, v, log_decay, state, *, slots=None, scale=None, o=None):
     if sd not in _IO:
         raise ValueError(f"state must be float32 or bfloat16, got {sd}")
     if o is None:
-        o, ro = _new_rows((B, H, dv), q)
+        o = q.new_empty((B, H, dv))
+        ro = capi.m3_rows_t(o.data_ptr(), H * dv, dv)
     elif o.shape != (B, H, dv):
         raise ValueError(f"o must be {(B, H, dv)}, got {tuple(o.shape)}")
     else:
         ro, _ = _rows(o, "o", io, dev)
     n = B if slots is None else state.shape[0]
     shape = capi.m3_linear_shape_t(B, B, 0, *heads, dk, dv, ion, _IO[sd], dk ** -0.5 if scale is None else scale)
-    rc = capi.m3_linear_decode_step(shape, rq, rk, rv, _decay(log_decay, H, dev), _index(slots, "slots", B, dev), n,
-                                    _pool(state, "state", (n, H, dk, dv), dev, sd), ro, _stream(dev))
+    rc = capi.m3_linear_decode_step(shape, rq, rk, rv, _ptr(log_decay, "log_decay", (H,), torch.float32, dev),
+                                    _ptr(slots, "slots", (B,), torch.int32, dev), n,
+                                    _ptr(state, "state", (n, H, dk, dv), sd, dev), ro, _stream(dev))
     if rc:
         raise capi.M3Error(rc, "m3_linear_decode_step")
     return o
@@ -256,16 +243,16 @@ def backward(q, k, v, log_decay, go, state=None, gfinal=None, *, cu_seqlens=None
         raise ValueError(f"state must be float32 or bfloat16, got {sd}")
     shape = capi.m3_linear_shape_t(batch, T, max_seqlen or longest, *heads, dk, dv, ion, _IO[sd],
                                    dk ** -0.5 if scale is None else scale)
-    (gq, rgq), (gk, rgk), (gv, rgv) = (_new_rows(t.shape, t) for t in (q, k, v))
+    (gq, rgq), (gk, rgk), (gv, rgv) = _like_rows(q, heads[0], dk), _like_rows(k, heads[1], dk), _like_rows(v, heads[2], dv)
     g = {"q": gq, "k": gk, "v": gv}
     pool = (batch, H, dk, dv)
     if state is not None:
         g["state"] = torch.empty(pool, device=q.device, dtype=torch.float32)
-    wp, wn, workspace = _workspace(workspace, capi.m3_linear_prefill_backward_workspace_bytes(shape), dev,
+    wp, wn, workspace = _workspace(workspace, capi.m3_linear_prefill_backward_workspace_bytes(shape), q, dev,
                                    "m3_linear_prefill_backward")
     rc = capi.m3_linear_prefill_backward(
-        shape, rq, rk, rv, _decay(log_decay, H, dev), cu, _pool(state, "state", pool, dev, sd), rg,
-        _pool(gfinal, "gfinal", pool, dev, torch.float32), rgq, rgk, rgv,
+        shape, rq, rk, rv, _ptr(log_decay, "log_decay", (H,), torch.float32, dev), cu,
+        _ptr(state, "state", pool, sd, dev), rg, _ptr(gfinal, "gfinal", pool, torch.float32, dev), rgq, rgk, rgv,
         g["state"].data_ptr() if state is not None else None, wp, wn, _stream(dev))
     if rc:
         raise capi.M3Error(rc, "m3_linear_prefill_backward")

@@ -15,8 +15,8 @@ from __future__ import annotations
 import torch
 
 from . import capi
-from .linear import _device, _new_rows, _on, _rows, _stream, _workspace
-from .mixer import _IO, _ptr
+from .linear import _device, _like_rows, _ptr, _rows, _stream, _workspace
+from .mixer import _IO
 
 
 def axes_table(inv_freq: torch.Tensor, sections, interleaved: bool = False) -> torch.Tensor:
@@ -42,18 +42,9 @@ def axes_table(inv_freq: torch.Tensor, sections, interleaved: bool = False) -> t
     return torch.where(pick, inv_freq, torch.zeros_like(inv_freq)).float().contiguous()
 
 
-def _weight(w, name, d, device):
-    if w is None:
-        return None
-    _on(w, name, device)
-    if w.shape != (d,):
-        raise ValueError(f"{name} must be [{d}], got {tuple(w.shape)}")
-    return _ptr(w, name, torch.float32)
-
-
-def _out(out, name, x, device):
+def _out(out, name, x, heads, d, device):
     if out is None:
-        return _new_rows(x.shape, x)
+        return _like_rows(x, heads, d)
     if out.shape != x.shape:
         raise ValueError("q_out and k_out must be shaped like q and k")
     return out, _rows(out, name, x.dtype, device)[0]
@@ -67,8 +58,6 @@ def _common(q, k, positions, inv_freq, norm, eps, halves):
     rk, (bk, Tk, hk, dk) = _rows(k, "k", io, dev)
     if bk != b or Tk != T or dk != d:
         raise ValueError(f"q and k must share tokens and channels: {tuple(q.shape)}, {tuple(k.shape)}")
-    _on(inv_freq, "inv_freq", dev)
-    _on(positions, "positions", dev)
     f, pd = inv_freq.shape, positions.dtype
     if len(f) not in (1, 2):
         raise ValueError(f"inv_freq must be [n] or [axes,n], got {tuple(f)}")
@@ -78,7 +67,8 @@ def _common(q, k, positions, inv_freq, norm, eps, halves):
     if positions.numel() != axes * T or (axes > 1 and positions.shape[0] != axes):
         raise ValueError(f"positions must be [{axes},{T}], got {tuple(positions.shape)}")
     shape = capi.m3_rotary_shape_t(T, hq, hk, d, 2 * f[-1], axes, _IO[io], pd is torch.int64, bool(halves), bool(norm), eps)
-    return dev, io, shape, rq, rk, _ptr(positions, "positions", None), _ptr(inv_freq, "inv_freq", torch.float32), d
+    return (dev, io, shape, rq, rk, _ptr(positions, "positions", None, pd, dev),
+            _ptr(inv_freq, "inv_freq", None, torch.float32, dev), hq, hk, d)
 
 
 def norm_rotate(q, k, positions, inv_freq, *, norm=True, eps=1e-6, q_weight=None, k_weight=None, halves=False,
@@ -86,11 +76,11 @@ def norm_rotate(q, k, positions, inv_freq, *, norm=True, eps=1e-6, q_weight=None
     """Returns (q', k'), shaped like q and k (new ones, or ``q_out`` and
     ``k_out``, which may be q and k themselves).  ``q_weight`` and ``k_weight``
     [D] float32 belong to the norm; norm=False only turns."""
-    dev, io, shape, rq, rk, pos, freq, d = _common(q, k, positions, inv_freq, norm, eps, halves)
-    q_out, ro = _out(q_out, "q_out", q, dev)
-    k_out, rko = _out(k_out, "k_out", k, dev)
-    rc = capi.m3_norm_rotate(shape, rq, rk, pos, freq, _weight(q_weight, "q_weight", d, dev),
-                             _weight(k_weight, "k_weight", d, dev), ro, rko, _stream(dev))
+    dev, io, shape, rq, rk, pos, freq, hq, hk, d = _common(q, k, positions, inv_freq, norm, eps, halves)
+    q_out, ro = _out(q_out, "q_out", q, hq, d, dev)
+    k_out, rko = _out(k_out, "k_out", k, hk, d, dev)
+    rc = capi.m3_norm_rotate(shape, rq, rk, pos, freq, _ptr(q_weight, "q_weight", (d,), torch.float32, dev),
+                             _ptr(k_weight, "k_weight", (d,), torch.float32, dev), ro, rko, _stream(dev))
     if rc:
         raise capi.M3Error(rc, "m3_norm_rotate")
     return q_out, k_out
@@ -100,20 +90,22 @@ def norm_rotate_backward(q, k, positions, inv_freq, gq, gk, *, norm=True, eps=1e
                          halves=False, workspace=None):
     """Gradients of sum(gq * q') + sum(gk * k') for q', k' = norm_rotate(q, k,
     ...): a dict of q and k, and q_weight and k_weight (float32) where given."""
-    dev, io, shape, rq, rk, pos, freq, d = _common(q, k, positions, inv_freq, norm, eps, halves)
+    dev, io, shape, rq, rk, pos, freq, hq, hk, d = _common(q, k, positions, inv_freq, norm, eps, halves)
     if gq.shape != q.shape or gk.shape != k.shape:
         raise ValueError("gq and gk must be shaped like q and k")
-    wp, wn, workspace = _workspace(workspace, capi.m3_norm_rotate_backward_workspace_bytes(shape), dev,
+    wp, wn, workspace = _workspace(workspace, capi.m3_norm_rotate_backward_workspace_bytes(shape), q, dev,
                                    "m3_norm_rotate_backward")
-    (dq, rdq), (dk, rdk) = _new_rows(q.shape, q), _new_rows(k.shape, k)
-    g = {"q": dq, "k": dk}
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            g[name] = torch.empty((d,), device=q.device, dtype=torch.float32)
-    rc = capi.m3_norm_rotate_backward(
-        shape, rq, rk, pos, freq, _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev),
-        _rows(gq, "gq", io, dev)[0], _rows(gk, "gk", io, dev)[0], rdq, rdk, *(g[n].data_ptr() if n in g else None for n in ("q_weight", "k_weight")),
-        wp, wn, _stream(dev))
+    pqw, pkw = _ptr(q_weight, "q_weight", (d,), torch.float32, dev), _ptr(k_weight, "k_weight", (d,), torch.float32, dev)
+    (dq, rdq), (dk, rdk) = _like_rows(q, hq, d), _like_rows(k, hk, d)
+    g, pdq, pdk = {"q": dq, "k": dk}, None, None
+    if q_weight is not None:
+        g["q_weight"] = torch.empty_like(q_weight)
+        pdq = g["q_weight"].data_ptr()
+    if k_weight is not None:
+        g["k_weight"] = torch.empty_like(k_weight)
+        pdk = g["k_weight"].data_ptr()
+    rc = capi.m3_norm_rotate_backward(shape, rq, rk, pos, freq, pqw, pkw, _rows(gq, "gq", io, dev)[0],
+                                      _rows(gk, "gk", io, dev)[0], rdq, rdk, pdq, pdk, wp, wn, _stream(dev))
     if rc:
         raise capi.M3Error(rc, "m3_norm_rotate_backward")
     return g

@@ -58,6 +58,26 @@ def test_linear_length_errors():
         assert call(_lshape(tokens=1 << 31)) == U
 
 
+def test_more_than_one_launch_takes():
+    # 2^32 threads: 256 x (3 scans x 2 column tiles) for each segment slot and head
+    one = dict(q_heads=1, k_heads=1, v_heads=1)
+    size = capi.m3_linear_prefill_workspace_bytes
+    assert size(_lshape(batch=2795682, tokens=0, **one)) > 0 and size(_lshape(batch=2795683, tokens=0, **one)) == 0
+    assert size(_lshape(batch=1, tokens=(1 << 31) - 1, **one)) > 0
+    assert size(_lshape(batch=1, tokens=(1 << 31) - 1, q_heads=2, k_heads=1, v_heads=1)) == 0
+    assert _prefill(_lshape(batch=2795683, tokens=0, **one)) == U and _backward(_lshape(batch=2795683, tokens=0, **one)) == U
+    # the slots that a plan may use stay within what is counted
+    for batch, tokens, heads in ((1, 256, 1000), (1, 4096, 32), (3, 300000, 1), (1, 520, 252), (40, 131072, 1), (1, 262144, 1)):
+        s = _lshape(batch=batch, tokens=tokens, q_heads=heads, k_heads=heads, v_heads=heads)
+        for L in capi.m3_linear_plan(s)[1:]:
+            assert ((tokens // L if L else 0) + batch) * heads <= (batch + 8 + tokens / 1024) * heads + 512
+    assert _decode(_lshape(batch=8388088, **one), n=1 << 23) == U
+    # a wave of 64 for each token's q and k
+    size = capi.m3_norm_rotate_backward_workspace_bytes
+    assert size(_rshape(tokens=33554429, q_heads=1, k_heads=1)) > 0 and size(_rshape(tokens=33554430, q_heads=1, k_heads=1)) == 0
+    assert size(_rshape(tokens=33554429, q_heads=33, k_heads=1)) == 0          # two waves of q
+
+
 @pytest.mark.parametrize("call,names", [("prefill", "qkvo"), ("decode", "qkvo"), ("backward", ("q", "k", "v", "go", "gq", "gk", "gv"))])
 def test_linear_row_errors(call, names):
     f = CALLS[call]
