@@ -259,8 +259,9 @@ bool out_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim) {
     return by_token || by_head;
 }
 
-// Columns of z a workgroup takes: fp32 I/O holds three planes of everything.
-int z_tile(int dz, bool f32) { return f32 ? std::min(m3::lin_tile(dz), 64) : m3::lin_tile(dz); }
+// Columns of z a workgroup takes, up to `most`: 64 with fp32 I/O, which holds three planes of everything.
+int z_tile(int dz, bool f32, int most = 128) { return std::min(m3::lin_tile(dz), std::min(most, f32 ? 64 : 128)); }
+int z_tiles(int dz, bool f32, int most = 128) { return (dz + z_tile(dz, f32, most) - 1) / z_tile(dz, f32, most); }
 
 // Tokens per segment, a power of two (0: sequences are not cut) for `scans` scans over `columns`
 // column tiles in one launch.
@@ -276,7 +277,9 @@ int64_t segment(const m3_linear_shape_t *s, int scans, int columns) {
     // sequences of 1024 x 32 x 128: 207 us with segments of 1024, 227 of 512, 240 of
     // 2048).  The gradients' scans differ more: four (4096 x 32 x 128 135 us, 148 with
     // two).  1024 tokens at most: 65536 x 64 x 64 703 us, 729 with 2048.
-    int64_t L = 256;
+    // From 256 on, or 128 of the slower fp32 rows (1000 x 8 x 128 34 us, 47 with 256;
+    // in bf16 2000 x 32 x 128 53 us, 45 with 256).
+    int64_t L = s->io_dtype == M3_DTYPE_F32 ? 128 : 256;
     while (L < 1024 && L * (scans > 1 ? 1024 : 512) < s->tokens * per) L *= 2;
     return longest > L ? L : 0;
 }
@@ -291,15 +294,29 @@ int64_t segment_slots(const m3_linear_shape_t *s, int64_t L) { return L ? s->tok
 
 struct Layout {
     int64_t L, slots;
+    int32_t most; // columns of z a workgroup takes at most
     int32_t fold; // few segments: each reads the slots before its own instead of a pass that joins them
     size_t seg_f, seg_b, part[3], total; // byte offsets: segment states forwards, backwards, the parts of gradients
 };
+// Narrower workgroups while there is at most one for each compute unit: the
+// chain of chunks is as long, but a chunk's work, and the state to load and
+// store, less.  77 x 16 x 128 12.1 us, 10.3 with 64 columns, 9.0 with 32;
+// 1000 x 32 x 128 38, 30, 34; gradients of 250 x 16 x 128 17.8, 12.7, 11.6.
+int most_columns(const m3_linear_shape_t *s, int64_t slots, const int *dz, int scans) {
+    const bool f32 = s->io_dtype == M3_DTYPE_F32;
+    int most = f32 ? 64 : 128;
+    for (; most > 32; most /= 2) {
+        int64_t columns = 0;
+        for (int i = 0; i < scans; ++i) columns += z_tiles(dz[i], f32, most / 2);
+        if (slots * heads(s) * columns > 256) break;
+    }
+    return most;
+}
 Layout prefill_layout(const m3_linear_shape_t *s) {
     Layout w{};
-    const bool f32 = s->io_dtype == M3_DTYPE_F32;
-    const int zt = z_tile(s->value_dim, f32);
-    w.L = segment(s, 1, (s->value_dim + zt - 1) / zt);
+    w.L = segment(s, 1, z_tiles(s->value_dim, s->io_dtype == M3_DTYPE_F32));
     w.slots = segment_slots(s, w.L);
+    w.most = most_columns(s, w.slots, &s->value_dim, 1);
     w.fold = few_segments(s, w.L);
     if (w.L) w.total = round_up(size_t(w.slots) * heads(s) * s->key_dim * s->value_dim * 4);
     w.total = std::max(w.total, kAlign);
@@ -310,6 +327,8 @@ Layout backward_layout(const m3_linear_shape_t *s) {
     const int32_t H = heads(s);
     w.L = segment(s, 3, 1);
     w.slots = segment_slots(s, w.L);
+    const int dz[3] = {s->key_dim, s->key_dim, s->value_dim};
+    w.most = most_columns(s, w.slots, dz, 3);
     w.fold = few_segments(s, w.L);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -330,10 +349,10 @@ Layout backward_layout(const m3_linear_shape_t *s) {
 }
 
 // Launches the scans p.role[0 .. n-1], which share their tile sizes.
-hipError_t launch_scan(LinParams p, bool f32, bool out, hipStream_t st) {
-    const int dx = m3::lin_tile(p.role[0].dx), dz = z_tile(p.role[0].dz, f32);
-    p.ztiles = (p.role[0].dz + dz - 1) / dz;
-    for (int i = 1; i < p.nroles; ++i) p.ztiles = std::max(p.ztiles, (p.role[i].dz + dz - 1) / dz);
+hipError_t launch_scan(LinParams p, bool f32, int most, bool out, hipStream_t st) {
+    const int dx = m3::lin_tile(p.role[0].dx), dz = z_tile(p.role[0].dz, f32, most);
+    p.ztiles = 1;
+    for (int i = 0; i < p.nroles; ++i) p.ztiles = std::max(p.ztiles, (p.role[i].dz + dz - 1) / dz);
     // heads that share rows, and more neighbours of them where that leaves 32
     // groups an XCD to spread: 65536 x 64 x 64 takes 681 us with 16 heads in a
     // group, 740 us with one; 16 ragged sequences of 32 heads of 128 176 us with
@@ -352,7 +371,7 @@ hipError_t launch_scan(LinParams p, bool f32, bool out, hipStream_t st) {
 }
 
 // The scans in as few launches as their tile sizes allow.
-hipError_t launch_scans(const LinParams &all, int n, bool f32, bool out, hipStream_t st) {
+hipError_t launch_scans(const LinParams &all, int n, bool f32, int most, bool out, hipStream_t st) {
     bool done[3] = {};
     for (int i = 0; i < n; ++i) {
         if (done[i]) continue;
@@ -360,11 +379,11 @@ hipError_t launch_scans(const LinParams &all, int n, bool f32, bool out, hipStre
         p.nroles = 0;
         for (int j = i; j < n; ++j)
             if (!done[j] && m3::lin_tile(all.role[j].dx) == m3::lin_tile(all.role[i].dx) &&
-                z_tile(all.role[j].dz, f32) == z_tile(all.role[i].dz, f32)) {
+                z_tile(all.role[j].dz, f32, most) == z_tile(all.role[i].dz, f32, most)) {
                 p.role[p.nroles++] = all.role[j];
                 done[j] = true;
             }
-        const hipError_t e = launch_scan(p, f32, out, st);
+        const hipError_t e = launch_scan(p, f32, most, out, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -474,10 +493,10 @@ m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q
     R.seg = static_cast<float *>(workspace);
     const bool f32 = shape->io_dtype == M3_DTYPE_F32;
     if (w.L) {
-        if (launch_scans(p, 1, f32, false, stream) != hipSuccess) return M3_ERR_HIP;
+        if (launch_scans(p, 1, f32, w.most, false, stream) != hipSuccess) return M3_ERR_HIP;
         if (!w.fold && launch_join(p, 1, stream) != hipSuccess) return M3_ERR_HIP;
     }
-    return launch_scans(p, 1, f32, true, stream) == hipSuccess ? M3_OK : M3_ERR_HIP;
+    return launch_scans(p, 1, f32, w.most, true, stream) == hipSuccess ? M3_OK : M3_ERR_HIP;
 }
 
 m3_status_t m3_linear_decode_step(const m3_linear_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
@@ -583,10 +602,10 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
         a.role[0].init = p.role[0].init;
         a.role[0].init16 = p.role[0].init16;
         a.role[1] = p.role[2];
-        if (launch_scans(a, 2, f32, false, stream) != hipSuccess) return M3_ERR_HIP;
+        if (launch_scans(a, 2, f32, w.most, false, stream) != hipSuccess) return M3_ERR_HIP;
         if (!w.fold && launch_join(a, 2, stream) != hipSuccess) return M3_ERR_HIP;
     }
-    if (launch_scans(p, 3, f32, true, stream) != hipSuccess) return M3_ERR_HIP;
+    if (launch_scans(p, 3, f32, w.most, true, stream) != hipSuccess) return M3_ERR_HIP;
     if (sums.n && T > 0) {
         sums.seq = p;
         const int64_t n = T * H * (std::max(dk, dv) / 8); // no row has more heads than H
