@@ -47,8 +47,9 @@
  * Ownership, streams, threads and errors are those of m3_ssm.h: the caller
  * owns every buffer and the workspace, calls only enqueue kernels, nothing is
  * allocated or synchronised, a workspace needs no initialisation and serves
- * one call at a time.  Outputs must not overlap inputs, except that
- * final_state may be init.
+ * one call at a time.  Outputs must not overlap inputs or each other, except
+ * that final_state may be init; M3_ERR_INVALID_ARGUMENT where one starts at
+ * another's address.
  */
 #ifndef M3_LINEAR_H
 #define M3_LINEAR_H
@@ -69,7 +70,8 @@ typedef struct {
 /* Supported: key_dim and value_dim multiples of 8 from 8 to 128; any head
  * counts that divide the largest; batch >= 1; tokens >= 0 (decode: ignored,
  * there is one token per sequence).  M3_ERR_INVALID_ARGUMENT for counts that
- * do not divide, M3_ERR_UNSUPPORTED for other sizes, and for more sequences,
+ * do not divide, M3_ERR_UNSUPPORTED for other sizes, for H times key_dim or
+ * value_dim from 2^24 on, and for more sequences,
  * tokens and heads than one launch has threads for: (batch + 8 + tokens / 1024)
  * H up to 2795690, for a decode step (batch + 8) H up to 8388095. */
 typedef struct {

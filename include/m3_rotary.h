@@ -15,7 +15,8 @@
  * Rows and strides are those of m3_linear.h (m3_rows_t: channels contiguous,
  * 16-byte aligned rows), and ownership, streams and errors those of m3_ssm.h.
  * An output's rows may be its own input's rows (same pointer and strides);
- * outputs overlap nothing else.
+ * outputs overlap nothing else (M3_ERR_INVALID_ARGUMENT where one starts at
+ * another operand's address).
  */
 #ifndef M3_ROTARY_H
 #define M3_ROTARY_H

@@ -230,7 +230,9 @@ m3_status_t check_shape(const m3_linear_shape_t *s, bool decode) {
     if (H % s->q_heads || H % s->k_heads || H % s->v_heads) return M3_ERR_INVALID_ARGUMENT;
     if (s->key_dim % 8 || s->value_dim % 8 || s->key_dim > 128 || s->value_dim > 128) return M3_ERR_UNSUPPORTED;
     // counts of sequences and tokens are indexed in 32 bits (cu_seqlens, slots), workgroups too
-    if (s->batch > (int64_t(1) << 31) - 2 || H > (1 << 20)) return M3_ERR_UNSUPPORTED;
+    if (s->batch > (int64_t(1) << 31) - 2) return M3_ERR_UNSUPPORTED;
+    // one token's rows of all heads, in parts of a gradient: a chunk of them within 2^32 bytes
+    if (int64_t(H) * std::max(s->key_dim, s->value_dim) >= int64_t(1) << 24) return M3_ERR_UNSUPPORTED;
     if (!decode && s->tokens > (int64_t(1) << 31) - 1) return M3_ERR_UNSUPPORTED;
     // a launch has fewer than 2^32 threads: workgroups of 256 for each head, two column
     // tiles and three scans of a segment slot: one per sequence, and one per 1024 tokens
@@ -257,6 +259,12 @@ bool out_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim) {
     const bool by_token = (tokens == 1 || t >= (heads - 1) * h + dim) && (heads == 1 || h >= dim);
     const bool by_head = (heads == 1 || h >= (tokens - 1) * t + dim) && (tokens == 1 || t >= dim);
     return by_token || by_head;
+}
+
+// An output that starts where another operand does (others may still overlap: views are not compared).
+template <typename... R>
+bool starts_in(const m3_rows_t *out, int64_t tokens, const R *...others) {
+    return tokens > 0 && ((out->data == others->data) || ...);
 }
 
 // Columns of z a workgroup takes, up to `most`: 64 with fp32 I/O, which holds three planes of everything.
@@ -472,6 +480,7 @@ m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q
     if (!aligned16(init) || !aligned16(final_state)) return M3_ERR_INVALID_ARGUMENT;
     const Layout w = prefill_layout(shape);
     if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return M3_ERR_WORKSPACE;
+    if (starts_in(o, shape->tokens, q, k, v)) return M3_ERR_INVALID_ARGUMENT;
 
     LinParams p = sequences(shape, cu_seqlens, slots, nstates, log_decay, w);
     LinRole &R = p.role[0];
@@ -512,6 +521,7 @@ m3_status_t m3_linear_decode_step(const m3_linear_shape_t *shape, const m3_rows_
     if (!log_decay || (reinterpret_cast<uintptr_t>(log_decay) & 3) || (reinterpret_cast<uintptr_t>(slots) & 3))
         return M3_ERR_INVALID_ARGUMENT;
     if (!state || !aligned16(state) || nstates < 0 || (!slots && nstates < shape->batch)) return M3_ERR_INVALID_ARGUMENT;
+    if (starts_in(o, shape->batch, q, k, v)) return M3_ERR_INVALID_ARGUMENT;
     m3::LinStepParams p{};
     p.q = q->data; p.qt = q->token_stride; p.qh = q->head_stride; p.qg = H / shape->q_heads;
     p.k = k->data; p.kt = k->token_stride; p.kh = k->head_stride; p.kg = H / shape->k_heads;
@@ -549,6 +559,9 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
     if (!aligned16(init) || !aligned16(gfinal) || !aligned16(ginit)) return M3_ERR_INVALID_ARGUMENT;
     const Layout w = backward_layout(shape);
     if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return M3_ERR_WORKSPACE;
+    if (starts_in(gq, T, q, k, v, go, gk, gv) || starts_in(gk, T, q, k, v, go, gv) || starts_in(gv, T, q, k, v, go))
+        return M3_ERR_INVALID_ARGUMENT;
+    if (ginit && (ginit == init || ginit == gfinal)) return M3_ERR_INVALID_ARGUMENT;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
 
     LinParams p = sequences(shape, cu_seqlens, nullptr, shape->batch, log_decay, w);

@@ -14,8 +14,9 @@ least a row's channels, so slices of one projection's output need no copy.
 Sequences are packed along T: ``cu_seqlens`` [B+1] int32 on the device gives
 sequence b the tokens cu_seqlens[b]:cu_seqlens[b+1] (empty ones included).
 Without it the rows are one sequence, or, given as [B,T,H,D], B sequences of T
-tokens.  ``max_seqlen`` (an int) helps to plan; the result does not depend on it
-beyond rounding.
+tokens.  Rows outside every sequence are not read, and their rows of o not
+written (undefined in a new one); their gradients are zero.  ``max_seqlen``
+(an int) helps to plan; the result does not depend on it beyond rounding.
 
 States are [n,H,Dk,Dv], float32 or bfloat16.  ``slots`` [B] int32 on the device
 names each sequence's state of a pool; a slot outside 0..n-1 marks padding,

@@ -126,6 +126,31 @@ def test_prefill_cut_sequences(io, lengths, state):
     _check_prefill(c)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(16, 24), (64, 64), (64, 128), (128, 64), (128, 128), (32, 104)])
+@pytest.mark.parametrize("lengths,heads", [([70, 1, 0, 33, 130], (6, 2, 6)), ([300, 0, 0, 270], (6, 6, 3))])
+def test_many_heads(io, dk, dv, lengths, heads):
+    """Workgroups enough for the widest column tiles, of whole sequences and cut
+    ones: ten times the same heads, which have to agree bit for bit."""
+    import copy
+    from mamba_selective_ssm_ssd_amd import capi, linear
+    c = Case(lengths, heads, dk, dv, io, seed=dk + dv, state=True)
+    many, n = copy.copy(c), 10
+    for name in ("q", "k", "v", "go", "state", "gfinal"):
+        setattr(many, name, getattr(c, name).repeat(1, n, *[1] * (getattr(c, name).dim() - 2)))
+    many.ld = c.ld.repeat(n)
+    rc, a, b = capi.m3_linear_plan(linear.make_shape(len(lengths), sum(lengths), *(n * h for h in heads), dk, dv, c.dt, max_seqlen=max(lengths)))
+    assert rc == 0 and (a > 0) == (b > 0) == (max(lengths) > 256)
+    o, final = _run_prefill(many, max_seqlen=max(lengths))
+    g = _run_backward(many, max_seqlen=max(lengths))
+    for t, h in ((o, 6), (final, 6), *((g[x], heads["qkv".index(x)]) for x in "qkv"), (g["state"], 6)):
+        assert all(torch.equal(t[:, i * h:(i + 1) * h], t[:, :h]) for i in range(1, n))
+    (wo, wf), (ao, af) = _oracle_prefill(c)
+    _check("o", o[:, :6], wo, ao, c.dt)
+    _check("final", final[:, :6], wf, af, torch.float32)
+    _compare_backward(c, {x: t[:, :heads["qkv".index(x)] if x != "state" else 6] for x, t in g.items()})
+
+
 @pytest.mark.parametrize("state", [False, True])
 def test_prefill_hint_changes_nothing_but_rounding(state):
     """max_seqlen is only a hint: too small, too large or absent."""
@@ -203,7 +228,10 @@ def _run_backward(c, **kw):
 
 
 def _check_backward(c, **kw):
-    g = _run_backward(c, **kw)
+    _compare_backward(c, _run_backward(c, **kw))
+
+
+def _compare_backward(c, g):
     pick = (lambda f: [None if t is None else f(_np(t)) for t in (c.state, c.gfinal)])
     want = ol.backward(*c.host(), _np(c.go), c.cu, *pick(lambda x: x))
     size = ol.backward(*c.host(True), np.abs(_np(c.go)), c.cu, *pick(np.abs))
@@ -398,6 +426,113 @@ def test_results_do_not_depend_on_the_run_or_the_neighbours():
     assert torch.equal(o0, o1) and torch.equal(f0, f1) and all(torch.equal(g0[n], g1[n]) for n in g0)
 
 
+def test_two_streams_at_once():
+    """Calls of two streams, each with a workspace of its own, beside each other."""
+    from mamba_selective_ssm_ssd_amd import linear
+    cases = [Case([900, 40, 700], (8, 4, 4), 64, 64, "bf16", seed=40, state=True), Case([1300], (6, 6, 6), 128, 128, "bf16", seed=41, state=True)]
+    want = [(_run_prefill(c), _run_backward(c)) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                final = torch.empty_like(c.state)
+                o, _ = linear.prefill(*c.args(), state=c.state, final=final, cu_seqlens=c.cu_dev)
+                g = linear.backward(*c.args(), c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev)
+                got[i].append((o, final, g))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for o, final, g in runs:
+            assert torch.equal(o, w[0][0]) and torch.equal(final, w[0][1]) and all(torch.equal(g[n], w[1][n]) for n in g)
+
+
+def test_two_graphs_that_share_a_workspace():
+    from mamba_selective_ssm_ssd_amd import linear
+    a = Case([900, 40], (4, 2, 2), 64, 64, "bf16", seed=42, state=True)
+    b = Case([500, 600], (2, 2, 2), 128, 64, "bf16", seed=43, state=True)
+    ws = torch.empty(max(linear.workspace_bytes(c.q, c.k, c.v, c.cu_dev, backward=r) for c in (a, b) for r in (False, True)),
+                     dtype=torch.uint8, device="cuda")
+
+    def work(c):
+        o, f = linear.prefill(*c.args(), state=c.state, final=torch.empty_like(c.state), cu_seqlens=c.cu_dev, workspace=ws)
+        return [o, f, *linear.backward(*c.args(), c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev, workspace=ws).values()]
+
+    want = [[t.clone() for t in work(c)] for c in (a, b)]
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    torch.cuda.synchronize()
+    for g, c in zip(graphs, (a, b)):
+        with torch.cuda.graph(g):
+            outs.append(work(c))
+    for _ in range(3):
+        for out in outs:
+            for t in out:
+                t.fill_(float("nan"))
+        ws.fill_(255)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for out, w in zip(outs, want) for x, y in zip(out, w))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_strides_broadcasts_and_a_start_behind_zero(io):
+    """Rows as [head][token][channel], heads broadcast by a stride of zero, sequences that start behind row 0."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([300, 20], (4, 2, 4), 64, 32, io, seed=44, state=True)
+    o0, f0 = _run_prefill(c)
+    g0 = _run_backward(c)
+    turn = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    o1 = torch.empty(4, 320, 32, device="cuda", dtype=c.dt).transpose(0, 1)
+    f1 = torch.empty_like(f0)
+    linear.prefill(turn(c.q), turn(c.k), turn(c.v), c.ld, state=c.state, final=f1, cu_seqlens=c.cu_dev, o=o1)
+    g1 = linear.backward(turn(c.q), turn(c.k), turn(c.v), c.ld, turn(c.go), state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev)
+    assert torch.equal(o0, o1) and torch.equal(f0, f1) and all(torch.equal(g0[n], g1[n]) for n in g0)
+    one = c.k[:, :1]
+    oa, _ = linear.prefill(c.q, one.expand(320, 4, 64), c.v, c.ld, cu_seqlens=c.cu_dev)
+    ob, _ = linear.prefill(c.q, one.repeat(1, 4, 1), c.v, c.ld, cu_seqlens=c.cu_dev)
+    assert torch.equal(oa, ob)
+    pad = lambda t: torch.cat([torch.full_like(t[:7], float("nan")), t, torch.full_like(t[:9], float("nan"))])  # noqa: E731
+    o2 = torch.full((336, 4, 32), 5.0, device="cuda", dtype=c.dt)
+    f2 = torch.empty_like(f0)
+    linear.prefill(pad(c.q), pad(c.k), pad(c.v), c.ld, state=c.state, final=f2, cu_seqlens=c.cu_dev + 7, o=o2)
+    # where a segment starts depends on the first row's number: up to rounding the same
+    (wo, wf), (ao, af) = _oracle_prefill(c)
+    _check("o", o2[7:327], wo, ao, c.dt)
+    _check("final", f2, wf, af, torch.float32)
+    assert (o2[:7] == 5).all() and (o2[327:] == 5).all()
+
+
+def test_no_tokens_at_all():
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([0, 0, 0], (4, 2, 1), 64, 32, "bf16", seed=45, state=True)
+    o, f = _run_prefill(c)
+    assert o.shape == (0, 4, 32) and torch.equal(f, c.state)
+    g = _run_backward(c)
+    assert g["k"].shape == (0, 2, 64) and torch.equal(g["state"], c.gfinal)
+    with pytest.raises(Exception):
+        linear.decode_step(*c.args(), c.state[:0])
+
+
+def test_states_larger_than_32_bits_count():
+    """A pool of more than 2^31 entries: the last states of it, prompt and step."""
+    from mamba_selective_ssm_ssd_amd import linear
+    n = (1 << 31) // (4 * 128 * 128) + 3
+    pool = torch.empty(n, 4, 128, 128, device="cuda")
+    c = Case([70, 40], (4, 2, 2), 128, 128, "bf16", seed=46, state=True)
+    slots = torch.tensor([n - 1, n - 2], dtype=torch.int32, device="cuda")
+    pool[[n - 1, n - 2]] = c.state
+    pool[[0, n - 3]] = 3.0
+    o, _ = linear.prefill(*c.args(), state=pool, cu_seqlens=c.cu_dev, slots=slots)
+    o1, f1 = _run_prefill(c)
+    assert torch.equal(o, o1) and torch.equal(pool[[n - 1, n - 2]], f1)
+    d = Case([1, 1], (4, 2, 2), 128, 128, "bf16", seed=47)
+    s = linear.decode_step(*d.args(), pool, slots=slots)
+    assert torch.equal(s, linear.decode_step(*d.args(), f1)) and torch.equal(pool[[n - 1, n - 2]], f1)
+    assert (pool[[0, n - 3]] == 3).all()
+
+
 def test_graph_capture_and_replay():
     from mamba_selective_ssm_ssd_amd import linear, rotary
     c = Case([600, 0, 300], (4, 2, 2), 64, 64, "bf16", seed=15, state=True)
@@ -457,5 +592,7 @@ def test_device_refusals():
         linear.prefill(c.q, c.k.float(), c.v, c.ld)
     with pytest.raises(ValueError):
         linear.backward(*c.args(), c.go[:5])
+    with pytest.raises(capi.M3Error):                                   # an output that is an input
+        linear.prefill(*c.args(), o=c.v)
     with pytest.raises(capi.M3Error):                                   # outputs that overlap themselves
         linear.prefill(*c.args(), o=torch.empty(1, 2, 64, device="cuda", dtype=torch.bfloat16).expand(10, 2, 64))

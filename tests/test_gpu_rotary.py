@@ -116,6 +116,36 @@ def test_norm_rotate_backward(case, io):
             assert bool((err <= tol).all())
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [
+    # rows enough that a wave takes several sets of one token, the last of them in part
+    (1100, 37, 3, 128, 128, 1, True, True, True, False, False, False),
+    (1100, 20, 20, 64, 32, 1, False, True, True, True, False, True),
+    (1100, 70, 1, 8, 8, 1, False, True, False, False, False, False),
+    (1100, 5, 2, 256, 128, 2, True, False, False, False, True, False)])
+def test_norm_rotate_many_rows(case, io):
+    test_norm_rotate(case, io)
+
+
+def test_heads_outside_tokens_and_no_keys():
+    """Rows as [head][token][channel], broadcast inputs, and queries alone."""
+    from mamba_selective_ssm_ssd_amd import rotary
+    q, k, pos, f, qw, kw = _setup(50, 4, 2, 64, 64, "bf16")
+    want = rotary.norm_rotate(q, k, pos, f, q_weight=qw, k_weight=kw)
+    turned = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k)]
+    outs = [torch.empty(h, 50, 64, device="cuda", dtype=q.dtype).transpose(0, 1) for h in (4, 2)]
+    rotary.norm_rotate(*turned, pos, f, q_weight=qw, k_weight=kw, q_out=outs[0], k_out=outs[1])
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    one = rotary.norm_rotate(q[:, :1].expand(50, 4, 64), k[:1].expand(50, 2, 64), pos, f)
+    full = rotary.norm_rotate(q[:, :1].repeat(1, 4, 1), k[:1].repeat(50, 1, 1), pos, f)
+    assert all(torch.equal(a, b) for a, b in zip(one, full))
+    y, none = rotary.norm_rotate(q, k[:, :0], pos, f, q_weight=qw)
+    assert torch.equal(y, want[0]) and none.shape == (50, 0, 64)
+    g = rotary.norm_rotate_backward(q, k[:, :0], pos, f, q, k[:, :0], q_weight=qw)
+    ref = rotary.norm_rotate_backward(q, k, pos, f, q, k, q_weight=qw, k_weight=kw)
+    assert torch.equal(g["q"], ref["q"]) and g["k"].shape == (50, 0, 64)
+
+
 def test_in_place_batches_and_far_rows():
     from mamba_selective_ssm_ssd_amd import rotary
     q, k, pos, f, qw, kw = _setup(60, 4, 2, 64, 64, "bf16")

@@ -129,6 +129,22 @@ def test_linear_plan_and_workspace():
     assert capi.m3_linear_plan(_lshape(batch=0))[0] == I
 
 
+def test_outputs_that_start_in_another_operand():
+    at = lambda h, d, n: _rows(h, d, data=n << 20)  # noqa: E731
+    fine = dict(q=at(4, 64, 1), k=at(2, 64, 2), v=at(1, 32, 3))
+    for n in "qkv":
+        assert _prefill(**fine, o=at(4, 32, "?qkv".index(n))) == I and _decode(**fine, o=at(4, 32, "?qkv".index(n))) == I
+    grads = dict(go=at(4, 32, 4), gq=at(4, 64, 5), gk=at(2, 64, 6), gv=at(1, 32, 7))
+    for n, (h, d) in dict(gq=(4, 64), gk=(2, 64), gv=(1, 32)).items():
+        for other in (1, 2, 3, 4, 5, 6, 7):
+            if other != list(grads).index(n) + 4:
+                assert _backward(**fine, **{**grads, n: at(h, d, other)}) == I, (n, other)
+    assert _backward(**fine, **grads, gfinal=FAKE, ginit=FAKE) == I and _backward(**fine, **grads, init=FAKE, ginit=FAKE) == I
+    # the heads' parts of one token beyond what a chunk's offsets count
+    big = _lshape(batch=1, tokens=1, q_heads=1 << 18, k_heads=1, v_heads=1)
+    assert _prefill(big) == U and capi.m3_linear_prefill_backward_workspace_bytes(big) == 0
+
+
 def _rshape(**kw):
     d = dict(tokens=10, q_heads=4, k_heads=2, dim=64, rot=32, axes=1, io_dtype=capi.M3_DTYPE_BF16, pos_int64=0, halves=0, norm=1, eps=1e-6)
     return capi.m3_rotary_shape_t(**{**d, **kw})
@@ -169,6 +185,17 @@ def test_rotary_backward_errors():
     assert _rotate_back(dqw=None) == I and _rotate_back(kw=None) == I and _rotate_back(dkw=FAKE + 2) == I
     assert _rotate_back(gq=_rows(4, 64, data=None)) == I and _rotate_back(gk=None) == I
     assert capi.m3_norm_rotate_backward_workspace_bytes(_rshape(tokens=0)) == 2 * 64 * 4
+
+
+def test_rotary_outputs_that_start_in_another_operand():
+    at = lambda h, n, **kw: _rows(h, 64, data=n << 20, **kw)  # noqa: E731
+    fine = dict(q=at(4, 1), k=at(2, 2), qo=at(4, 3), ko=at(2, 4))
+    bad = [dict(qo=at(4, 2)), dict(ko=at(2, 1)), dict(ko=at(2, 3)), dict(qo=at(4, 1, token_stride=512)), dict(ko=at(2, 2, head_stride=96, token_stride=192))]
+    for b in bad:
+        assert _rotate(**{**fine, **b}) == I, b
+        assert _rotate_back(**{**fine, **b}, gq=at(4, 5), gk=at(2, 6)) == I, b
+    for b in (dict(qo=at(4, 6)), dict(ko=at(2, 5)), dict(qo=at(4, 5, head_stride=128, token_stride=512))):
+        assert _rotate_back(**{**fine, **b}, gq=at(4, 5), gk=at(2, 6)) == I, b
 
 
 def test_rotary_nothing_to_do():
