@@ -6,7 +6,8 @@
 // A lane's channels are four rotation pairs whichever way the pairs lie, and
 // they are the same pairs in every row: a wave takes up to kRows sets of rows
 // of one token and forms the four angles' sine and cosine once for all of
-// them.  Bound by reading and writing the rows.
+// them.  Bound by reading and writing the rows: 16384 x 40 x 128 in bf16 54 us
+// (6.2 TB/s); a few rows take 3 us, the time of a launch.
 #include "m3_rotary.h"
 #include "m3_device.hpp"
 
@@ -180,6 +181,8 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
 //     dw = sum gn r x,    dx = r w gn - (r^3 / dim) x sum(x w gn).
 // Workgroups are q's or k's, walk their items with a fixed stride and keep their
 // share of dw in registers; k_norm_rotate_sum adds the shares in a fixed order.
+// Bound by its rows: 8192 x 128 x 64 in bf16 73 us (5.5 TB/s), 3001 x 20 x 96 in
+// fp32 17.5 us (4.0 TB/s).
 template <typename IO, int LPR, bool HALVES>
 __global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams p) {
     constexpr int RPW = 64 / LPR, NW = kRT / 64;
@@ -258,7 +261,8 @@ __global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams
 }
 
 // Sum of the workgroups' shares, four channels of one weight per workgroup: a
-// share to a thread, then the threads of a wave and the waves in pairs.
+// share to a thread, then the threads of a wave and the waves in turn.  4 us for
+// 1024 shares of 64 channels: the latency of a load, the sums and the launch.
 __global__ __launch_bounds__(1024) void k_norm_rotate_sum(const float *part, int split, int n, int dim, float *dq, float *dk) {
     __shared__ floatx4 s[16];
     const int c = blockIdx.x * 4;
