@@ -186,6 +186,9 @@ template <typename IO, int DX, int DZ, bool OUT>
 struct LinCfg {
     static constexpr bool F32 = std::is_same<IO, float>::value;
     static constexpr int PL = F32 ? 3 : 1;
+    // planes of the weights: a row of a few tokens is the sum of a few of them, so a
+    // bf16 result would show one plane's rounding whole, beside its own
+    static constexpr int WP = F32 ? 3 : 2;
     static constexpr int Q = F32 || (OUT && DX == 128 && DZ == 128) ? 32 : 64; // 64 rows of 128 x 128 spill (442 us for 219)
     static constexpr int MP = DX / 32, NP = DZ / 32; // 32 x 32 blocks of the state, 16 x 16 tiles in pairs
     // the state's tiles over the waves: MW along x (MTW tiles each, a pair of
@@ -608,7 +611,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, O
         load();
 
         floatx4 O[C::NOT]; // out^T, tile j: channel z0 + 16 tile(j) + 4 g + v of row 16 rt + r16
-        lfrag<PL> pf[KS];  // weights of the chunk's rows in row 16 rt + r16
+        lfrag<C::WP> pf[KS]; // weights of the chunk's rows in row 16 rt + r16
         if (OUT) {
             lfrag<PL> xf[C::MP];
 #pragma unroll
@@ -626,11 +629,10 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, O
                 float pr[8];
 #pragma unroll
                 for (int v = 0; v < 8; ++v) pr[v] = a[v >> 2][v & 3] * inner[2 * s + (v >> 2)][v & 3];
-                // the weights of a bf16 result are rounded to bf16, as above
-                pf[s] = lsplit<PL>(pr);
+                pf[s] = lsplit<C::WP>(pr);
                 const uint32_t at0 = 2 * s == rt ? ~0u : 0u, all0 = 2 * s < rt ? ~0u : 0u, at1 = 2 * s + 1 == rt ? ~0u : 0u, all1 = 2 * s + 1 < rt ? ~0u : 0u;
 #pragma unroll
-                for (int k = 0; k < PL; ++k) {
+                for (int k = 0; k < C::WP; ++k) {
                     const uint4 u = __builtin_bit_cast(uint4, pf[s].v[k]);
                     pf[s].v[k] = bf16x8_from_words(u.x & ((upto[0] & at0) | all0), u.y & ((upto[1] & at0) | all0),
                                                    u.z & ((upto[0] & at1) | all1), u.w & ((upto[1] & at1) | all1));
@@ -682,7 +684,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, O
                 for (int q = 0; q < NB; ++q)
                     if (j0 + q < C::NTW || (OUT && j0 + q < C::NOT)) zf[q] = lin_zcol<PL, DZ, C::ZP>(zs, 2 * s, tile(j0 + q), r16, g);
                 if (OUT)
-                    lpairs<PL, PL>([&](auto a, auto b) {
+                    lpairs<PL, C::WP>([&](auto a, auto b) {
 #pragma unroll
                         for (int q = 0; q < NB; ++q)
                             if (j0 + q < C::NOT)

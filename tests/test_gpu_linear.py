@@ -3,10 +3,9 @@ oracle (oracle/linear.py): prompt pass, gradients, single-token step.
 
 Tolerances.  Running the recurrence on absolute values gives, for every entry
 of a result, the sum A of the sizes of its terms.  With bf16 I/O a term meets
-two roundings of at most 2^-8 that do not both reach it (the weight q.k of its
-own chunk, or the entry of the chunk's starting state), and the result one
-more, so |error| <= 2^-8 (A + |o|) up to second order; as independent errors
-the two have a norm of at most 2^-8 sqrt(2/3) of the terms'.  fp32 results
+at most one rounding of 2^-8 (of the entry of the chunk's starting state; the
+weights q.k of its own chunk are held to 2^-17), and the result one more, so
+|error| <= 2^-8 (A + |o|) up to second order.  fp32 results
 (states, and everything with fp32 I/O) add about Dk + Dv + 64 + the number of
 chunks terms in fp32, with decay factors of a few steps: at most 512 x 2^-24 A
 for these sizes.
@@ -107,6 +106,24 @@ def test_prefill_sizes(io, dk, dv):
 @pytest.mark.parametrize("n", [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200])
 def test_prefill_lengths(io, n):
     _check_prefill(Case([n], (2, 1, 2), 64, 32, io, seed=n, state=n % 2 == 1), max_seqlen=n)
+
+
+@pytest.mark.parametrize("dk,dv", [(16, 24), (64, 64), (128, 128), (64, 128), (128, 32)])
+@pytest.mark.parametrize("heads", [(2, 2, 2), (320, 320, 320)])
+def test_few_tokens_round_once(dk, dv, heads):
+    """Within a chunk the weights are held to 2^-17: without a state to start
+    from, a bf16 result and its gradients meet one rounding, the result's own."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([1, 2, 5], heads, dk, dv, "bf16", seed=dk + heads[0])
+    o, _ = linear.prefill(*c.args(), cu_seqlens=c.cu_dev, max_seqlen=5)
+    g = linear.backward(*c.args(), c.go, cu_seqlens=c.cu_dev, max_seqlen=5)
+    want, size = [ol.prefill(*c.host(a), c.cu, None)[0] for a in (False, True)]
+    wg = ol.backward(*c.host(), _np(c.go), c.cu, None, None)
+    sg = ol.backward(*c.host(True), np.abs(_np(c.go)), c.cu, None, None)
+    for name, got, w, a in (("o", o, want, size), *(("d" + n, g[n], wg[i], sg[i]) for i, n in enumerate("qkv"))):
+        over = np.abs(_np(got) - w) / (1.01 * U16 * np.abs(w) + (2.0 ** -16 + U32) * a + 1e-30)
+        print(f"{name}: {float(over.max()):.3f} of the bound", flush=True)
+        assert float(over.max()) <= 1.0, name
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
