@@ -140,7 +140,8 @@ def _workspace(workspace, need: int, like: torch.Tensor, device: int, where: str
 
 
 def workspace_bytes(q, k, v, cu_seqlens=None, max_seqlen=0, backward=False) -> int:
-    """Bytes of the workspace that ``prefill`` (or ``backward``) takes for these operands."""
+    """Bytes of the workspace that ``prefill`` (or ``backward``) takes for these
+    operands, and the same max_seqlen."""
     dev, io, ion, _, _, _, b, T, heads, dk, dv = _operands(q, k, v)
     batch, _, longest = _sequences(b, T, cu_seqlens, dev)
     shape = make_shape(batch, T, *heads, dk, dv, io, max_seqlen=max_seqlen or longest)

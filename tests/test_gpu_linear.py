@@ -521,6 +521,35 @@ def test_strides_broadcasts_and_a_start_behind_zero(io):
     assert (o2[:7] == 5).all() and (o2[327:] == 5).all()
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_rows_as_far_apart_as_strides_go(io):
+    """The widest stride of tokens: a chunk spans 2 GiB, all rows many."""
+    from mamba_selective_ssm_ssd_amd import linear, rotary
+    T, H, D, wide = 270, 2, 64, (1 << 24) - 8
+    c = Case([T], (H, H, H), D, D, io, seed=48, state=True)
+    flat = torch.empty((T - 1) * wide + 6 * H * D, device="cuda", dtype=c.dt)
+
+    def far(i, t=None):
+        v = flat[i * H * D:].as_strided((T, H, D), (wide, D, 1))
+        if t is not None:
+            v.copy_(t)
+        return v
+
+    q, k, v, go, o = far(0, c.q), far(1, c.k), far(2, c.v), far(3, c.go), far(4)
+    want, final = _run_prefill(c)
+    got, f = linear.prefill(q, k, v, c.ld, state=c.state, final=torch.empty_like(final), o=o)
+    assert torch.equal(got, want) and torch.equal(f, final)
+    ref = _run_backward(c)
+    g = linear.backward(q, k, v, c.ld, go, state=c.state, gfinal=c.gfinal)
+    assert all(torch.equal(g[n], ref[n]) for n in ref)
+    pos, freq = torch.arange(T, device="cuda", dtype=torch.int32), torch.linspace(1, 0.01, 32, device="cuda")
+    a = rotary.norm_rotate(c.q, c.k, pos, freq)
+    b = rotary.norm_rotate(q, k, pos, freq, q_out=q, k_out=k)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(v, c.v) and torch.equal(go, c.go)
+    with pytest.raises(Exception):
+        linear.prefill(flat.as_strided((2, H, D), (1 << 24, D, 1)), c.k[:2], c.v[:2], c.ld)
+
+
 def test_no_tokens_at_all():
     from mamba_selective_ssm_ssd_amd import linear
     c = Case([0, 0, 0], (4, 2, 1), 64, 32, "bf16", seed=45, state=True)
