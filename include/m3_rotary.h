@@ -10,7 +10,9 @@
  * and channels from rot on are not turned.  Several axes (time, height, width)
  * are rows of inv_freq: an axis has its frequencies at the pairs it turns and
  * zeros elsewhere.  Arithmetic is fp32 with angles in fp64, taken modulo a
- * turn; every output is rounded once.
+ * turn; every output is rounded once.  mean(x^2) + eps has to be a normal fp32
+ * number: eps may be 0, but then a row of zeros gives NaN, and so does the
+ * gradient of its weight.
  *
  * Rows and strides are those of m3_linear.h (m3_rows_t: channels contiguous,
  * 16-byte aligned rows), and ownership, streams and errors those of m3_ssm.h.

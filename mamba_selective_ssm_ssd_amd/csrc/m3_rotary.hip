@@ -225,7 +225,8 @@ __global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams
                 if (on) rx[i].unpack(v);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
-                const float r = __builtin_amdgcn_rsqf(fmaf(row_sum<LPR>(ss), p.inv_dim, p.eps));
+                // without a row nothing joins dw: eps may be 0, and then r would be infinite
+                const float rms = __builtin_amdgcn_rsqf(fmaf(row_sum<LPR>(ss), p.inv_dim, p.eps)), r = on ? rms : 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     dw[c] = fmaf(a[c] * r, v[c], dw[c]);

@@ -194,3 +194,30 @@ def test_refusals():
         a = dict(q=q, k=k, positions=pos, inv_freq=f) | bad
         with pytest.raises(ValueError):
             rotary.norm_rotate(a.pop("q"), a.pop("k"), a.pop("positions"), a.pop("inv_freq"), **a)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("eps", [0.0, 1e-40])
+@pytest.mark.parametrize("T,hq,hk,D,rot,halves", [(7, 5, 3, 64, 64, True), (40, 1, 2, 96, 48, False), (2500, 3, 9, 64, 32, True),
+                                                 (9, 7, 1, 8, 8, False), (3, 3, 5, 256, 256, True)])
+def test_norm_without_eps_and_sets_of_rows_in_part(T, hq, hk, D, rot, halves, eps, io):
+    """No eps, and head counts that leave a wave's last set of rows in part: the
+    places of no row must not reach the weights' gradients."""
+    from mamba_selective_ssm_ssd_amd import rotary
+    q, k, pos, f, qw, kw = _setup(T, hq, hk, D, rot, io, seed=D)
+    gq, gk = (torch.randn(x.shape, generator=torch.Generator().manual_seed(i)).to(DT[io]).cuda() for i, x in enumerate((q, k)))
+    y = rotary.norm_rotate(q, k, pos, f, eps=eps, q_weight=qw, k_weight=kw, halves=halves)
+    got = rotary.norm_rotate_backward(q, k, pos, f, gq, gk, eps=eps, q_weight=qw, k_weight=kw, halves=halves)
+    r16 = 1.01 * 2.0 ** -8 if io == "bf16" else 0
+    for n, x, g, w, out in (("q", q, gq, qw, y[0]), ("k", k, gk, kw, y[1])):
+        x, g, w = _np(x), _np(g), _np(w)
+        want = ol.norm_rotate(x, _np(pos), _np(f), w, True, eps, halves)
+        # rows of normal numbers: their mean of squares is far above eps, so _size's own eps changes nothing here
+        assert np.mean(x * x, -1).min() > 1e-3
+        assert (np.abs(_np(out) - want) <= 16 * E * 1.001 * _size(x, _np(pos), _np(f), w, True, halves) + r16 * np.abs(want)).all()
+        dx, dw = ol.norm_rotate_backward(x, _np(pos), _np(f), g, w, True, eps, halves)
+        gn, a = _size(g, _np(pos), _np(f), None, False, halves), np.abs(x)
+        r = 1 / np.sqrt(np.mean(a * a, -1, keepdims=True) + eps)
+        size = r * gn * np.abs(w) + r ** 3 * a * np.mean(a * gn * np.abs(w), -1, keepdims=True)
+        assert (np.abs(_np(got[n]) - dx) <= 64 * E * size + r16 * np.abs(dx)).all()
+        assert (np.abs(_np(got[n + "_weight"]) - dw) <= 128 * E * np.sum(gn * a * r, axis=(0, 1))).all()
