@@ -4,6 +4,7 @@
 // states, the sum of a shared row's gradients, the single-token step.
 #include "m3_linear.h"
 #include "k_linear.hpp"
+#include "lin_plan.hpp"
 #include "m3_internal.hpp"
 
 #include <algorithm>
@@ -365,16 +366,9 @@ hipError_t launch_scan(LinParams p, bool f32, int most, bool out, hipStream_t st
     const int dx = m3::lin_tile(p.role[0].dx), dz = z_tile(p.role[0].dz, f32, most);
     p.ztiles = 1;
     for (int i = 0; i < p.nroles; ++i) p.ztiles = std::max(p.ztiles, (p.role[i].dz + dz - 1) / dz);
-    // Heads that share rows, and more neighbours of them: their rows lie side by
-    // side in memory.  Up to 16 where that leaves 32 groups an XCD to spread: 65536
-    // x 64 x 64 takes 703 us, 780 with one; 16 ragged sequences of 32 heads of 128
-    // 228 us with 16, 208 with one.  Several scans of whole sequences, which are of
-    // like lengths, up to eight and two groups an XCD: gradients of 4 x 2048 x 64 x
-    // 64 147 us, 161 with one; of cut ones 232, 217 with no more than share rows.
-    p.hg = 1;
-    for (int i = 0; i < p.nroles; ++i) p.hg = std::max(p.hg, std::max(p.role[i].xg, std::max(p.role[i].yg, p.role[i].zg)));
-    const int widest = p.nroles == 1 ? 16 : p.segbits ? 1 : 8, least = 8 * (p.nroles == 1 ? 32 : 2);
-    while (p.hg < widest && p.H % (2 * p.hg) == 0 && p.nseg * (p.H / (2 * p.hg)) >= least) p.hg *= 2;
+    int32_t share = 1; // heads that have a row in common
+    for (int i = 0; i < p.nroles; ++i) share = std::max(share, std::max(p.role[i].xg, std::max(p.role[i].yg, p.role[i].zg)));
+    p.hg = m3::lin_head_group(share, p.H, p.nseg, p.ztiles, p.nroles, p.segbits != 0);
     p.group = p.hg * p.ztiles * p.nroles;
     p.nwork = int32_t((p.nseg * (p.H / p.hg) + 7) / 8 * 8 * p.group);
     switch (dx) {

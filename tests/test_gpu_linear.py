@@ -642,3 +642,13 @@ def test_device_refusals():
         linear.prefill(*c.args(), o=c.v)
     with pytest.raises(capi.M3Error):                                   # outputs that overlap themselves
         linear.prefill(*c.args(), o=torch.empty(1, 2, 64, device="cuda", dtype=torch.bfloat16).expand(10, 2, 64))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,heads,dk,dv", [([200], (64, 1, 1), 128, 128), ([130, 70], (24, 3, 3), 64, 128), ([1, 0, 90], (1, 30, 1), 32, 40),
+                                                 ([600], (32, 1, 4), 64, 64)])
+def test_many_heads_of_one_row(io, lengths, heads, dk, dv):
+    """Few sequences whose heads share rows: workgroups of one row on several XCDs."""
+    c = Case(lengths, heads, dk, dv, io, seed=60, state=True)
+    _check_prefill(c, max_seqlen=max(lengths))
+    _check_backward(c, max_seqlen=max(lengths))
