@@ -8,6 +8,7 @@
 #include "m3_internal.hpp"
 
 #include <algorithm>
+#include <initializer_list>
 
 namespace m3 {
 
@@ -266,10 +267,17 @@ bool out_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim) {
     return by_token || by_head;
 }
 
-// An output that starts where another operand does (others may still overlap: views are not compared).
-template <typename... R>
-bool starts_in(const m3_rows_t *out, int64_t tokens, const R *...others) {
-    return tokens > 0 && ((out->data == others->data) || ...);
+// Where rows start (nowhere without a token).
+const void *start(const m3_rows_t *r, int64_t tokens) { return tokens > 0 ? r->data : nullptr; }
+// Whether one of the first `outputs` operands starts where another operand does (they may
+// still overlap: views are not compared).  Absent ones are null.
+bool starts_in(int outputs, std::initializer_list<const void *> operands) {
+    const void *const *p = operands.begin();
+    const int n = int(operands.size());
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (p[i] && p[i] == p[j]) return true;
+    return false;
 }
 
 // Columns of z a workgroup takes, up to `most`: 64 with fp32 I/O, which holds three planes of everything.
@@ -481,7 +489,11 @@ m3_status_t m3_linear_prefill(const m3_linear_shape_t *shape, const m3_rows_t *q
     if (!aligned16(init) || !aligned16(final_state)) return M3_ERR_INVALID_ARGUMENT;
     const Layout w = prefill_layout(shape);
     if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return M3_ERR_WORKSPACE;
-    if (starts_in(o, shape->tokens, q, k, v)) return M3_ERR_INVALID_ARGUMENT;
+    const int64_t T = shape->tokens;
+    if (starts_in(3, {start(o, T), final_state, workspace, start(q, T), start(k, T), start(v, T), log_decay, cu_seqlens, slots,
+                      init == final_state ? nullptr : init}) ||
+        starts_in(1, {init, start(o, T), workspace}))
+        return M3_ERR_INVALID_ARGUMENT;
 
     LinParams p = sequences(shape, cu_seqlens, slots, nstates, log_decay, w);
     LinRole &R = p.role[0];
@@ -522,7 +534,7 @@ m3_status_t m3_linear_decode_step(const m3_linear_shape_t *shape, const m3_rows_
     if (!log_decay || (reinterpret_cast<uintptr_t>(log_decay) & 3) || (reinterpret_cast<uintptr_t>(slots) & 3))
         return M3_ERR_INVALID_ARGUMENT;
     if (!state || !aligned16(state) || nstates < 0 || (!slots && nstates < shape->batch)) return M3_ERR_INVALID_ARGUMENT;
-    if (starts_in(o, shape->batch, q, k, v)) return M3_ERR_INVALID_ARGUMENT;
+    if (starts_in(2, {o->data, state, q->data, k->data, v->data, log_decay, slots})) return M3_ERR_INVALID_ARGUMENT;
     m3::LinStepParams p{};
     p.q = q->data; p.qt = q->token_stride; p.qh = q->head_stride; p.qg = H / shape->q_heads;
     p.k = k->data; p.kt = k->token_stride; p.kh = k->head_stride; p.kg = H / shape->k_heads;
@@ -560,9 +572,9 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
     if (!aligned16(init) || !aligned16(gfinal) || !aligned16(ginit)) return M3_ERR_INVALID_ARGUMENT;
     const Layout w = backward_layout(shape);
     if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return M3_ERR_WORKSPACE;
-    if (starts_in(gq, T, q, k, v, go, gk, gv) || starts_in(gk, T, q, k, v, go, gv) || starts_in(gv, T, q, k, v, go))
+    if (starts_in(5, {start(gq, T), start(gk, T), start(gv, T), ginit, workspace, start(q, T), start(k, T), start(v, T), start(go, T),
+                      log_decay, cu_seqlens, init, gfinal}))
         return M3_ERR_INVALID_ARGUMENT;
-    if (ginit && (ginit == init || ginit == gfinal)) return M3_ERR_INVALID_ARGUMENT;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
 
     LinParams p = sequences(shape, cu_seqlens, nullptr, shape->batch, log_decay, w);

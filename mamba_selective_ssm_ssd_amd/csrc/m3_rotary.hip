@@ -12,6 +12,7 @@
 #include "m3_device.hpp"
 
 #include <algorithm>
+#include <initializer_list>
 
 namespace m3 {
 
@@ -370,17 +371,18 @@ bool rows_ok(const m3_rows_t *r, int64_t tokens, int32_t heads, int32_t dim, boo
     return by_token || by_head;
 }
 
-// Whether an output starts where another's rows do, or its own input's lie otherwise.
-bool outputs_overlap(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_rows_t *k, const m3_rows_t *qo,
-                     const m3_rows_t *ko, const m3_rows_t *gq, const m3_rows_t *gk) {
+// Whether an output's rows start where another operand does, or its own input's lie otherwise.
+bool rows_overlap(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_rows_t *k, const m3_rows_t *qo, const m3_rows_t *ko,
+                  const m3_rows_t *gq, const m3_rows_t *gk, std::initializer_list<const void *> others) {
     if (s->tokens == 0) return false;
     auto clash = [&](const m3_rows_t *out, const m3_rows_t *own, int32_t heads) {
         return own && out->data == own->data &&
                ((s->tokens > 1 && out->token_stride != own->token_stride) || (heads > 1 && out->head_stride != own->head_stride));
     };
-    if (clash(qo, q, s->q_heads) || clash(qo, gq, s->q_heads)) return true;
+    auto among = [&](const m3_rows_t *out) { return std::find(others.begin(), others.end(), out->data) != others.end(); };
+    if (clash(qo, q, s->q_heads) || clash(qo, gq, s->q_heads) || among(qo)) return true;
     if (s->k_heads == 0) return false;
-    if (clash(ko, k, s->k_heads) || clash(ko, gk, s->k_heads)) return true;
+    if (clash(ko, k, s->k_heads) || clash(ko, gk, s->k_heads) || among(ko)) return true;
     return qo->data == ko->data || qo->data == k->data || ko->data == q->data ||
            (gq && (qo->data == gk->data || ko->data == gq->data));
 }
@@ -452,7 +454,8 @@ m3_status_t m3_norm_rotate(const m3_rotary_shape_t *shape, const m3_rows_t *q, c
         !rows_ok(q_out, T, shape->q_heads, shape->dim, true) || !rows_ok(k_out, T, shape->k_heads, shape->dim, true))
         return M3_ERR_INVALID_ARGUMENT;
     if (T == 0) return M3_OK;
-    if (outputs_overlap(shape, q, k, q_out, k_out, nullptr, nullptr)) return M3_ERR_INVALID_ARGUMENT;
+    if (rows_overlap(shape, q, k, q_out, k_out, nullptr, nullptr, {positions, inv_freq, q_weight, k_weight}))
+        return M3_ERR_INVALID_ARGUMENT;
     m3::RotParams p = params(shape, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out);
     const int64_t grid = (T * (p.r[0].items + p.r[1].items) + 3) / 4;
     const hipError_t e = shape->io_dtype == M3_DTYPE_F32 ? m3::launch_rotary_io<float>(p, shape->halves, grid, false, stream)
@@ -484,7 +487,15 @@ m3_status_t m3_norm_rotate_backward(const m3_rotary_shape_t *shape, const m3_row
     if ((reinterpret_cast<uintptr_t>(dq_weight) & 3) || (reinterpret_cast<uintptr_t>(dk_weight) & 3)) return M3_ERR_INVALID_ARGUMENT;
     if (!workspace || !aligned16(workspace) || workspace_bytes < m3_norm_rotate_backward_workspace_bytes(shape))
         return M3_ERR_WORKSPACE;
-    if (outputs_overlap(shape, q, k, dq, dk, gq, gk)) return M3_ERR_INVALID_ARGUMENT;
+    if (rows_overlap(shape, q, k, dq, dk, gq, gk, {positions, inv_freq, q_weight, k_weight, dq_weight, dk_weight, workspace}))
+        return M3_ERR_INVALID_ARGUMENT;
+    // the weights' gradients and the workspace, each against every operand that is not a row of the gradients
+    const void *const small[] = {dq_weight, dk_weight, workspace, q_weight, k_weight, inv_freq, T ? positions : nullptr,
+                                 T ? q->data : nullptr, T ? gq->data : nullptr, T && shape->k_heads ? k->data : nullptr,
+                                 T && shape->k_heads ? gk->data : nullptr};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 11; ++j)
+            if (small[i] && small[i] == small[j]) return M3_ERR_INVALID_ARGUMENT;
     m3::RotParams p = params(shape, q, k, positions, inv_freq, q_weight, k_weight, dq, dk);
     p.r[0].g = gq->data; p.r[0].gt = gq->token_stride; p.r[0].gh = gq->head_stride;
     if (shape->k_heads) { p.r[1].g = gk->data; p.r[1].gt = gk->token_stride; p.r[1].gh = gk->head_stride; }

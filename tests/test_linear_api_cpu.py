@@ -227,3 +227,31 @@ def test_axes_table():
     with pytest.raises(ValueError):
         rotary.axes_table(f, (2, 3))
     assert ctypes.sizeof(capi.m3_rows_t) == 24
+
+
+def test_every_output_against_every_operand():
+    def call(f, heads, addresses, **kw):
+        return f(**kw, **{n: _rows(*heads[n], data=p) if n in heads else p for n, p in addresses.items()})
+
+    h = dict(q=(4, 64), k=(2, 64), v=(1, 32), o=(4, 32), go=(4, 32), gq=(4, 64), gk=(2, 64), gv=(1, 32), qo=(4, 64), ko=(2, 64))
+    r = {**h, "gq": (4, 64), "gk": (2, 64)}
+    for f, heads, names, outputs, may in (
+            (_prefill, h, "q k v o ld cu slots init fin ws", "o fin ws", {("fin", "init")}),
+            (_decode, h, "q k v o ld slots state", "o state", set()),
+            (_backward, h, "q k v go gq gk gv ld cu init gfinal ginit ws", "gq gk gv ginit ws", set()),
+            (_rotate, r, "q k qo ko pos freq qw kw", "qo ko", {("qo", "q"), ("ko", "k")}),
+            (_rotate_back, r, "q k gq gk qo ko pos freq qw kw dqw dkw ws", "qo ko dqw dkw ws",
+             {("qo", "q"), ("qo", "gq"), ("ko", "k"), ("ko", "gk")})):
+        names = names.split()
+        at = {n: (i + 1) << 20 for i, n in enumerate(names)}
+        for out in outputs.split():
+            for other in names:
+                if out != other and (out, other) not in may:
+                    assert call(f, heads, {**at, out: at[other]}) == I, (f.__name__, out, other)
+
+
+def test_operands_without_a_token_are_not_compared():
+    # rows of no token may point anywhere; the other operands are compared all the same
+    s = _rshape(tokens=0)
+    assert _rotate(s, pos=None, qw=FAKE, kw=FAKE) == OK
+    assert _rotate_back(s, dqw=2 * FAKE, dkw=2 * FAKE, ws=3 * FAKE) == I and _rotate_back(s, dqw=2 * FAKE, dkw=3 * FAKE, ws=3 * FAKE) == I
