@@ -31,8 +31,9 @@
  * States are [n][H][key_dim][value_dim], contiguous, 16-byte aligned, in
  * state_dtype (arithmetic is fp32; bf16 is rounded to nearest even once per
  * call).  slots (device, int32, batch entries, or NULL: sequence b has state
- * b) names each sequence's state among the nstates of the pool.  A sequence
- * whose slot is negative or not below nstates is padding: nothing of it is
+ * b) names each sequence's state among the nstates of the pool (where no state
+ * is read or written, any count that the slots stay below).  A sequence whose
+ * slot is negative or not below nstates is padding: nothing of it is
  * read, and its rows of o are left as they were.  When two sequences of one
  * call name the same slot, the first has it; the rows of o of the later ones
  * are filled with NaN.

@@ -19,9 +19,10 @@ written (undefined in a new one); their gradients are zero.  ``max_seqlen``
 (an int) helps to plan; the result does not depend on it beyond rounding.
 
 States are [n,H,Dk,Dv], float32 or bfloat16.  ``slots`` [B] int32 on the device
-names each sequence's state of a pool; a slot outside 0..n-1 marks padding,
-whose outputs and state are left as they were; where sequences of one call
-share a slot, the first has it and the others' outputs are NaN.
+names each sequence's state of a pool; a slot outside 0..n-1 (without a pool: a
+negative one) marks padding, whose outputs and state are left as they were;
+where sequences of one call share a slot, the first has it and the others'
+outputs are NaN.
 
 As with ``mixer``, torch only holds memory and names the current stream; all
 tensors must be on the current device.
@@ -173,9 +174,8 @@ def prefill(q, k, v, log_decay, state=None, final=None, want_final=True, *, cu_s
         if state is None and slots is not None:
             raise ValueError("slots need a state pool: give final, or want_final=False")
         final = state if state is not None else torch.empty((batch, H, dk, dv), device=q.device, dtype=sd)
-    n = batch
-    if slots is not None and (state is not None or final is not None):
-        n = (state if state is not None else final).shape[0]
+    # without a pool any slot from 0 on is one of its own
+    n = batch if slots is None else given.shape[0] if given is not None else 1 << 31
     shape = capi.m3_linear_shape_t(batch, T, max_seqlen or longest, *heads, dk, dv, ion, _IO[sd],
                                    dk ** -0.5 if scale is None else scale)
     out_shape = (T, H, dv) if b is None else (b, T // b if b else 0, H, dv)

@@ -652,3 +652,22 @@ def test_many_heads_of_one_row(io, lengths, heads, dk, dv):
     c = Case(lengths, heads, dk, dv, io, seed=60, state=True)
     _check_prefill(c, max_seqlen=max(lengths))
     _check_backward(c, max_seqlen=max(lengths))
+
+
+@pytest.mark.parametrize("lengths", [[40, 30, 70], [400, 300, 700]])
+def test_prefill_slots_without_a_state(lengths):
+    """Slots of a batch that asks for no states: each sequence has its outputs
+    whatever its slot's number, padding and repeated slots as ever."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case(lengths, (2, 2, 2), 64, 64, "bf16", seed=61)
+    want, _ = linear.prefill(*c.args(), cu_seqlens=c.cu_dev, want_final=False)
+    for slots, pool in (([7, 900, 3], None), ([2 ** 31 - 1, 0, 5], None), ([8, 0, 3], 9)):
+        o = torch.full_like(want, 7.0)
+        final = None if pool is None else torch.full((pool, 2, 64, 64), 5.0, device="cuda")
+        linear.prefill(*c.args(), final=final, cu_seqlens=c.cu_dev, want_final=False, o=o,
+                       slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+        assert torch.equal(o, want) and (final is None or (final == 5).all())
+    o = torch.full_like(want, 7.0)
+    linear.prefill(*c.args(), cu_seqlens=c.cu_dev, want_final=False, o=o, slots=torch.tensor([-3, 40, 40], dtype=torch.int32, device="cuda"))
+    a, b = c.cu[1], c.cu[2]
+    assert (o[:a] == 7).all() and torch.equal(o[a:b], want[a:b]) and torch.isnan(o[b:].float()).all()
