@@ -43,7 +43,9 @@
  * fp32 from it, and no gradient is formed for it.  A non-finite value of one
  * token reaches, within its sequence and head, the outputs of its own chunk
  * (at most 64 tokens; counted from the end of the sequence for the gradients
- * of k and v) and of everything behind it, and no other sequence.
+ * of k and v) and of everything behind it, and no other sequence.  It may
+ * arrive as NaN where it was an infinity; an infinite entry of a state stays
+ * one, or becomes NaN where the decay of a chunk is zero in fp32.
  *
  * Ownership, streams, threads and errors are those of m3_ssm.h: the caller
  * owns every buffer and the workspace, calls only enqueue kernels, nothing is

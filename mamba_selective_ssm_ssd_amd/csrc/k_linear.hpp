@@ -348,6 +348,8 @@ __device__ __forceinline__ float lin_power(float ld2, int n) { return n > 0 ? __
 
 // s g^n, rounded once.  A slow decay is taken as s + s (g^n - 1): g^n itself,
 // rounded to 24 bits, would err the same way in every chunk of a long sequence.
+// Of an infinite s that sum makes inf - inf: such a result is s again, an
+// infinity as the product is, or the NaN that it was.
 struct LinDecay {
     float f;
     uint32_t keep; // all of s, or nothing, to add
@@ -357,7 +359,8 @@ struct LinDecay {
         keep = x > -0.5f ? 0xffffffffu : 0u;
     }
     __device__ __forceinline__ float operator()(float s) const {
-        return fmaf(s, f, __uint_as_float(__float_as_uint(s) & keep));
+        const float r = fmaf(s, f, __uint_as_float(__float_as_uint(s) & keep));
+        return r != r ? s : r;
     }
 };
 

@@ -671,3 +671,56 @@ def test_prefill_slots_without_a_state(lengths):
     linear.prefill(*c.args(), cu_seqlens=c.cu_dev, want_final=False, o=o, slots=torch.tensor([-3, 40, 40], dtype=torch.int32, device="cuda"))
     a, b = c.cu[1], c.cu[2]
     assert (o[:a] == 7).all() and torch.equal(o[a:b], want[a:b]) and torch.isnan(o[b:].float()).all()
+
+
+INF_DECAYS = [0.0, -1e-6, -0.01, -0.3, -0.6]
+
+
+def _infinite(state):
+    """The same states with an infinity of each sign in column 5 of every head, and where they are."""
+    s = state.clone()
+    s[:, :, 3, 5], s[:, :, 9, 5] = float("inf"), float("-inf")
+    at = torch.zeros_like(s, dtype=torch.bool)
+    at[:, :, 3, 5] = at[:, :, 9, 5] = True
+    return s, at
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("sd", ["f32", "bf16"])
+def test_step_keeps_infinite_states(io, sd):
+    """exp(log_decay) inf is inf, without any decay too; nothing else moves."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([1] * 3, (5, 5, 5), 32, 40, io, seed=62)
+    c.ld[:] = torch.tensor(INF_DECAYS)
+    s0 = torch.randn(3, 5, 32, 40, device="cuda").to(DT[sd])
+    s1, at = _infinite(s0)
+    o0 = linear.decode_step(*c.args(), s0)
+    o1 = linear.decode_step(*c.args(), s1)
+    assert torch.equal(s1[~at], s0[~at])
+    assert (s1[:, :, 3, 5] == float("inf")).all() and (s1[:, :, 9, 5] == float("-inf")).all()
+    keep = torch.arange(40, device="cuda") != 5
+    assert torch.equal(o1[..., keep], o0[..., keep])
+    # q[3] inf - q[9] inf: an infinity where their signs differ
+    a, b = c.q[..., 3].float(), c.q[..., 9].float()
+    want = a * float("inf") + b * float("-inf")
+    got, nan = o1[..., 5].float(), torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [40, 700, 2600])
+def test_prompt_keeps_infinite_states(io, n):
+    """The same of whole sequences, of a few segments folded and of many joined."""
+    from mamba_selective_ssm_ssd_amd import capi, linear
+    c = Case([n], (5, 5, 5), 32, 40, io, seed=63, state=True)
+    # decays that leave more than nothing behind the prompt
+    c.ld[:] = torch.tensor([0.0, -1e-6, -1e-4, -1e-3, -0.01])
+    rc, seg, _ = capi.m3_linear_plan(linear.make_shape(1, n, 5, 5, 5, 32, 40, c.dt))
+    assert rc == 0 and (seg == 0 if n == 40 else n <= 4 * seg if n == 700 and io == "bf16" else n > 4 * seg)
+    o0, f0 = _run_prefill(c)
+    c.state, at = _infinite(c.state)
+    o1, f1 = _run_prefill(c)
+    assert torch.equal(f1[~at], f0[~at])
+    assert (f1[:, :, 3, 5] == float("inf")).all() and (f1[:, :, 9, 5] == float("-inf")).all()
+    keep = torch.arange(40, device="cuda") != 5
+    assert torch.equal(o1[..., keep], o0[..., keep]) and not torch.isfinite(o1[..., 5].float()).any()
