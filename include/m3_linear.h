@@ -130,6 +130,8 @@ size_t m3_linear_prefill_backward_workspace_bytes(const m3_linear_shape_t *shape
  *            a row that several heads share are summed in fp32.  Rows of tokens
  *            outside every sequence are set to zero.
  *   ginit    gradient of init, like gfinal, or NULL: not written.
+ *            Where it is asked for, bf16 gradients of rows may be rounded
+ *            otherwise in their last bit.
  */
 m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
                                        const m3_rows_t *v, const float *log_decay, const int32_t *cu_seqlens,

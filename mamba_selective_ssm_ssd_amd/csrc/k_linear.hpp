@@ -63,6 +63,7 @@ struct LinParams {
     int32_t hg, group;       // heads that share rows; workgroups that do: hg x ztiles x nroles
     int32_t tail;            // extra workgroups per scan that zero the rows outside every sequence
     int32_t nwork;           // workgroups without the tail
+    int32_t grad;            // the scans are gradients
     int64_t batch, tokens, each; // each: tokens of a sequence without cu
     const int32_t *cu;       // null: equal sequences
     const int32_t *slots;    // null: sequence b has state b
@@ -412,7 +413,9 @@ __device__ __forceinline__ const LinParams &lin_args() {
 // The scan.  OUT: outputs (and the final state); otherwise only the state that
 // a segment's own rows leave, for the slot of the next segment.  UP: planes of
 // the weighted y that join the state; three keep it to fp32 accuracy, two (2^-17)
-// do where it is only rounded to bf16 and not handed out.
+// do where it is only rounded to bf16 and never handed out: in the gradients.  A
+// prompt takes three whether its final state is asked for or not, so that its
+// outputs are the same bits.
 template <typename IO, int DX, int DZ, bool OUT, int UP>
 __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, OUT>::WAVES)) void k_linear_scan(const LinParams p) {
     typedef LinCfg<IO, DX, DZ, OUT> C;
@@ -760,11 +763,11 @@ hipError_t launch_linear_planes(const LinParams &p, hipStream_t s) {
 
 template <typename IO, int DX, int DZ, bool OUT>
 hipError_t launch_linear_inst(const LinParams &p, hipStream_t s) {
-    // gradients of 4 x 2048 x 64 x 64: 168 us with two planes, 174 with three
+    // gradients of 4 x 2048 x 64 x 64: 144 us with two planes, 153 with three
     if constexpr (OUT && !std::is_same<IO, float>::value) {
-        bool fin = false;
-        for (int i = 0; i < p.nroles; ++i) fin |= p.role[i].fin != nullptr;
-        if (!fin) return launch_linear_planes<IO, DX, DZ, OUT, 2>(p, s);
+        bool three = !p.grad;
+        for (int i = 0; i < p.nroles; ++i) three |= p.role[i].fin != nullptr;
+        if (!three) return launch_linear_planes<IO, DX, DZ, OUT, 2>(p, s);
     }
     return launch_linear_planes<IO, DX, DZ, OUT, 3>(p, s);
 }

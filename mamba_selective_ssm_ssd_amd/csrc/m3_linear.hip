@@ -579,6 +579,7 @@ m3_status_t m3_linear_prefill_backward(const m3_linear_shape_t *shape, const m3_
 
     LinParams p = sequences(shape, cu_seqlens, nullptr, shape->batch, log_decay, w);
     p.tail = cu_seqlens ? 64 : 0;
+    p.grad = 1;
     const Rows rq{q, shape->q_heads, shape->key_dim}, rk{k, shape->k_heads, shape->key_dim}, rv{v, shape->v_heads, shape->value_dim}, rg{go, H, dv};
     const Rows x[3] = {rg, rv, rk}, y[3] = {rv, rg, rq}, z[3] = {rk, rq, rg};
     const m3_rows_t *out[3] = {gq, gk, gv};

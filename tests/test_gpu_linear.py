@@ -724,3 +724,16 @@ def test_prompt_keeps_infinite_states(io, n):
     assert (f1[:, :, 3, 5] == float("inf")).all() and (f1[:, :, 9, 5] == float("-inf")).all()
     keep = torch.arange(40, device="cuda") != 5
     assert torch.equal(o1[..., keep], o0[..., keep]) and not torch.isfinite(o1[..., 5].float()).any()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(32, 32), (64, 64), (128, 128), (64, 128)])
+@pytest.mark.parametrize("lengths", [[150, 3], [900, 200]])
+def test_outputs_do_not_depend_on_the_final_state(lengths, dk, dv, io):
+    """Bit for bit: with the final state, without it, and in place."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case(lengths, (3, 3, 3), dk, dv, io, seed=64, state=True)
+    o0, _ = _run_prefill(c)
+    o1, none = linear.prefill(*c.args(), state=c.state, cu_seqlens=c.cu_dev, want_final=False)
+    o2, _ = linear.prefill(*c.args(), state=c.state.clone(), cu_seqlens=c.cu_dev)
+    assert none is None and torch.equal(o0, o1) and torch.equal(o0, o2)
