@@ -91,7 +91,11 @@ typedef struct {
 /* Bytes of device workspace m3_linear_prefill needs (0: invalid or unsupported
  * shape).  Where the sequences and heads alone do not fill the chip, sequences
  * are cut into segments, and the workspace holds one fp32 state per segment
- * and head; otherwise it is 256 bytes, unused. */
+ * and head; otherwise it is 256 bytes, unused.  With L tokens a segment
+ * (m3_linear_plan) that is at most the smaller of tokens / L + batch and
+ * 2 tokens / L states of every head.  Without max_seqlen one sequence may be
+ * all tokens, so that batches are cut that need not be: 256 sequences of 2048
+ * tokens of 64 x 128 x 128 then take 3.2 GB, with it 256 bytes. */
 size_t m3_linear_prefill_workspace_bytes(const m3_linear_shape_t *shape);
 
 /* Tokens per segment of the prompt pass (0: sequences are not cut), and of the

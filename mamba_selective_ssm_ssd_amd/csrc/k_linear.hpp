@@ -54,7 +54,7 @@ struct LinRole {
     void *fin;               // state pool, or null: not written
     int32_t init16, fin16;   // the pools' entries are bf16
     int32_t sm, sn;          // strides of the state's two axes (pools and seg alike)
-    float *seg;              // [segment slot][H][dx dz] fp32, for the start of each segment of a cut sequence
+    float *seg;              // [state slot][H][dx dz] fp32, for the start of each segment of a cut sequence
 };
 
 struct LinParams {
@@ -72,6 +72,7 @@ struct LinParams {
     int32_t segbits;         // log2 of the tokens per segment, 0: sequences are not cut
     int32_t fold;            // slots hold what each segment leaves, not yet joined
     int64_t nseg;            // segment slots (batch when not cut)
+    int32_t sparse;          // states are kept for cut sequences alone
 };
 
 // First token of sequence b, clamped to the rows there are.
@@ -101,6 +102,15 @@ __device__ __forceinline__ int64_t lin_slot(const int32_t *slots, int64_t nstate
 // of two sequences never meet, there are at most tokens / L + batch of them,
 // and the sequence of a slot is found by bisection without any table.
 __device__ __forceinline__ int64_t lin_first_slot(const LinParams &p, int64_t b) { return (lin_start(p, b) >> p.segbits) + b; }
+
+// Where the states of sequence b's segments lie: at their slots, or, where there
+// are more sequences than segments of tokens, from 2 start / L on.  Only a cut
+// sequence, of n > L tokens, has states, and floor(2 (start + n) / L) -
+// floor(2 start / L) >= floor(2 n / L) >= ceil(n / L): two never meet, and there
+// are at most 2 tokens / L, however many sequences.
+__device__ __forceinline__ int64_t lin_state_slot(const LinParams &p, int64_t b, int64_t start) {
+    return p.sparse ? 2 * start >> p.segbits : (start >> p.segbits) + b;
+}
 
 // ---------------------------------------------------------------------------
 // Operands as PL planes of bf16 whose sum is the value: one plane for bf16
@@ -529,7 +539,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, O
     // hold what the segments left, each without those before it where they are
     // still to be folded.
     const bool cut = p.segbits && !(first && last);
-    const int64_t seg_at = (slot * p.H + h) * int64_t(area);
+    const int64_t seg_at = ((lin_state_slot(p, b, start) + (pos >> p.segbits)) * p.H + h) * int64_t(area);
     if (OUT && cut && (!first || R.init)) {
         const int64_t from = OUT && p.fold && !first ? (pos >> p.segbits) - 1 : 0; // slots before this one to fold in
         LinBuf s0(R.seg + seg_at - from * p.H * int64_t(area), area * 4);
@@ -741,7 +751,7 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, O
         const LinBuf s(static_cast<bf16 *>(R.fin) + (pool * p.H + h) * int64_t(area), area * 2);
         each([&](float v, uint32_t at) { s.put16(2 * at, v); return v; });
     } else {
-        const LinBuf s((OUT ? static_cast<float *>(R.fin) + (pool * p.H + h) * int64_t(area) : R.seg + ((slot + 1) * p.H + h) * int64_t(area)),
+        const LinBuf s((OUT ? static_cast<float *>(R.fin) + (pool * p.H + h) * int64_t(area) : R.seg + seg_at + p.H * int64_t(area)),
                        area * 4);
         each([&](float v, uint32_t at) { s.put(4 * at, v); return v; });
     }

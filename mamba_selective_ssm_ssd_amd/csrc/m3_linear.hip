@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const LinParams p) {
     if (lin_slot(p.slots, p.nstates, b) < 0) return;
     const int64_t area = int64_t(R.dx) * R.dz, e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
     if (e >= area) return;
-    float *w = R.seg + (lin_first_slot(p, b) * p.H + h) * area + e;
+    float *w = R.seg + (lin_state_slot(p, b, start) * p.H + h) * area + e;
     const int64_t step = p.H * area;
     floatx4 s = *reinterpret_cast<const floatx4 *>(w + step);
     const LinDecay d(p.log_decay[h], double(int64_t(1) << p.segbits));
@@ -312,6 +312,13 @@ int32_t few_segments(const m3_linear_shape_t *s, int64_t L) {
     return L && longest <= 4 * L;
 }
 int64_t segment_slots(const m3_linear_shape_t *s, int64_t L) { return L ? s->tokens / L + s->batch : s->batch; }
+// States of segments that a workspace holds: one a slot, or, with more sequences than segments of
+// tokens, those of cut sequences alone: 1000 sequences of 60000 tokens, the longest of 8192, take 235
+// states of every head instead of 1117.
+bool sparse_states(const m3_linear_shape_t *s, int64_t L) { return L && s->tokens / L < s->batch; }
+int64_t state_slots(const m3_linear_shape_t *s, int64_t L) {
+    return sparse_states(s, L) ? 2 * s->tokens / L : segment_slots(s, L);
+}
 
 struct Layout {
     int64_t L, slots;
@@ -339,7 +346,7 @@ Layout prefill_layout(const m3_linear_shape_t *s) {
     w.slots = segment_slots(s, w.L);
     w.most = most_columns(s, w.slots, &s->value_dim, 1);
     w.fold = few_segments(s, w.L);
-    if (w.L) w.total = round_up(size_t(w.slots) * heads(s) * s->key_dim * s->value_dim * 4);
+    if (w.L) w.total = round_up(size_t(state_slots(s, w.L)) * heads(s) * s->key_dim * s->value_dim * 4);
     w.total = std::max(w.total, kAlign);
     return w;
 }
@@ -358,7 +365,7 @@ Layout backward_layout(const m3_linear_shape_t *s) {
         return o;
     };
     if (w.L) {
-        const size_t n = size_t(w.slots) * H * s->key_dim * s->value_dim * 4;
+        const size_t n = size_t(state_slots(s, w.L)) * H * s->key_dim * s->value_dim * 4;
         w.seg_f = take(n);
         w.seg_b = take(n);
     }
@@ -440,6 +447,7 @@ LinParams sequences(const m3_linear_shape_t *s, const int32_t *cu, const int32_t
     p.fold = w.fold;
     while (p.segbits < 30 && w.L >> p.segbits > 1) ++p.segbits;
     p.nseg = w.slots;
+    p.sparse = sparse_states(s, w.L);
     return p;
 }
 

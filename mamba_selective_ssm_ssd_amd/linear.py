@@ -16,7 +16,10 @@ sequence b the tokens cu_seqlens[b]:cu_seqlens[b+1] (empty ones included).
 Without it the rows are one sequence, or, given as [B,T,H,D], B sequences of T
 tokens.  Rows outside every sequence are not read, and their rows of o not
 written (undefined in a new one); their gradients are zero.  ``max_seqlen``
-(an int) helps to plan; the result does not depend on it beyond rounding.
+(an int) helps to plan; the result does not depend on it beyond rounding.  Give
+it where sequences are many: without it one of them may be all of T, and enough
+of them to fill the chip are cut into segments all the same, with a workspace of
+an fp32 state per segment and head, and k and v read twice.
 
 States are [n,H,Dk,Dv], float32 or bfloat16.  ``slots`` [B] int32 on the device
 names each sequence's state of a pool; a slot outside 0..n-1 (without a pool: a

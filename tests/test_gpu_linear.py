@@ -737,3 +737,22 @@ def test_outputs_do_not_depend_on_the_final_state(lengths, dk, dv, io):
     o1, none = linear.prefill(*c.args(), state=c.state, cu_seqlens=c.cu_dev, want_final=False)
     o2, _ = linear.prefill(*c.args(), state=c.state.clone(), cu_seqlens=c.cu_dev)
     assert none is None and torch.equal(o0, o1) and torch.equal(o0, o2)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(32, 40), (128, 128)])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("long", [[257, 256, 513], [1500], [129, 128, 300, 700, 256, 257]])
+def test_many_short_sequences_and_a_few_cut_ones(long, state, dk, dv, io):
+    """More sequences than segments of tokens: states are kept for the cut ones
+    alone, whichever they are, in a workspace of garbage."""
+    from mamba_selective_ssm_ssd_amd import capi, linear
+    r = np.random.RandomState(len(long))
+    lengths = [int(n) for n in r.permutation([0, 0, 1, *r.randint(1, 30, 40), *long])]
+    c = Case(lengths, (2, 1, 2), dk, dv, io, seed=65, state=state)
+    T, B = sum(lengths), len(lengths)
+    for back in (False, True):
+        ws = torch.full((linear.workspace_bytes(c.q, c.k, c.v, c.cu_dev, backward=back),), 255, dtype=torch.uint8, device="cuda")
+        L = capi.m3_linear_plan(linear.make_shape(B, T, 2, 1, 2, dk, dv, c.dt))[1 + back]
+        assert 0 < L < max(lengths) and T // L < B
+        (_check_backward if back else _check_prefill)(c, workspace=ws)

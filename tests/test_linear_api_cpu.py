@@ -255,3 +255,15 @@ def test_operands_without_a_token_are_not_compared():
     s = _rshape(tokens=0)
     assert _rotate(s, pos=None, qw=FAKE, kw=FAKE) == OK
     assert _rotate_back(s, dqw=2 * FAKE, dkw=2 * FAKE, ws=3 * FAKE) == I and _rotate_back(s, dqw=2 * FAKE, dkw=3 * FAKE, ws=3 * FAKE) == I
+
+
+def test_workspace_of_many_sequences():
+    """States of segments are kept for cut sequences: at most 2 tokens / L, however many sequences there are."""
+    for batch, tokens, longest, heads in ((1000, 60000, 8192, 32), (256, 128000, 0, 64), (5000, 20000, 1000, 4), (300, 300 * 257, 0, 8),
+                                          (7, 4999, 0, 32), (40, 9000, 8000, 2)):
+        s = _lshape(batch=batch, tokens=tokens, max_seqlen=longest, q_heads=heads, k_heads=heads, v_heads=heads, key_dim=128, value_dim=128)
+        rc, a, b = capi.m3_linear_plan(s)
+        assert rc == OK and a > 0 and b > 0
+        for L, n, size in ((a, 1, capi.m3_linear_prefill_workspace_bytes), (b, 2, capi.m3_linear_prefill_backward_workspace_bytes)):
+            states = min(tokens // L + batch, max(2 * tokens // L, 1))
+            assert size(s) <= n * (states * heads * 128 * 128 * 4 + 256), (batch, tokens, L)
