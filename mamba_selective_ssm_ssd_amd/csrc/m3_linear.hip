@@ -313,8 +313,8 @@ int32_t few_segments(const m3_linear_shape_t *s, int64_t L) {
 }
 int64_t segment_slots(const m3_linear_shape_t *s, int64_t L) { return L ? s->tokens / L + s->batch : s->batch; }
 // States of segments that a workspace holds: one a slot, or, with more sequences than segments of
-// tokens, those of cut sequences alone: 1000 sequences of 60000 tokens, the longest of 8192, take 235
-// states of every head instead of 1117.
+// tokens, those of cut sequences alone: 1000 sequences of 60000 tokens, the longest of 8192, take 117
+// states of every head (245 MB of 32 x 128 x 128) instead of 1058.
 bool sparse_states(const m3_linear_shape_t *s, int64_t L) { return L && s->tokens / L < s->batch; }
 int64_t state_slots(const m3_linear_shape_t *s, int64_t L) {
     return sparse_states(s, L) ? 2 * s->tokens / L : segment_slots(s, L);
