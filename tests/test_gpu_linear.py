@@ -756,3 +756,55 @@ def test_many_short_sequences_and_a_few_cut_ones(long, state, dk, dv, io):
         L = capi.m3_linear_plan(linear.make_shape(B, T, 2, 1, 2, dk, dv, c.dt))[1 + back]
         assert 0 < L < max(lengths) and T // L < B
         (_check_backward if back else _check_prefill)(c, workspace=ws)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, -0.3, 0.0])
+@pytest.mark.parametrize("lengths", [[70, 1, 0, 33], [700, 300], [1500]])
+def test_scale(lengths, scale, io):
+    """A factor of its own through the prompt, its gradients (the states' among
+    them) and the step, of whole sequences, few segments and many."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case(lengths, (4, 2, 2), 64, 32, io, seed=66, state=True)
+    final = torch.empty_like(c.state)
+    o, _ = linear.prefill(*c.args(), state=c.state, final=final, cu_seqlens=c.cu_dev, scale=scale)
+    wo, wf = ol.prefill(*c.host(), c.cu, _np(c.state), scale)
+    ao, af = ol.prefill(*c.host(True), c.cu, np.abs(_np(c.state)), abs(scale))
+    _check("o", o, wo, ao, c.dt)
+    _check("final", final, wf, af, torch.float32)
+    g = linear.backward(*c.args(), c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev, scale=scale)
+    want = ol.backward(*c.host(), _np(c.go), c.cu, _np(c.state), _np(c.gfinal), scale)
+    size = ol.backward(*c.host(True), np.abs(_np(c.go)), c.cu, np.abs(_np(c.state)), np.abs(_np(c.gfinal)), abs(scale))
+    for n, w, a in zip(("q", "k", "v", "state"), want, size):
+        _check("d" + n, g[n], w, a, c.dt if n != "state" else torch.float32)
+    d = Case([1, 1], (4, 2, 2), 64, 32, io, seed=67, state=True)
+    pool = d.state.clone()
+    got = linear.decode_step(*d.args(), pool, scale=scale)
+    wo, wf = ol.prefill(*d.host(), d.cu, _np(d.state), scale)
+    ao, af = ol.prefill(*d.host(True), d.cu, np.abs(_np(d.state)), abs(scale))
+    assert (np.abs(_np(got) - wo) <= U32 * ao + (1.01 * U16 * np.abs(wo) if io == "bf16" else 0)).all()
+    _check("state", pool, wf, af, torch.float32)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 96), (24, 64)])
+@pytest.mark.parametrize("lengths", [[70, 1, 0, 33], [700, 0, 300], [1500]])
+def test_backward_from_bf16_states(lengths, dk, dv, io):
+    """Initial states in bf16, of whole sequences, few segments and many: the gradient of one is fp32."""
+    _check_backward(Case(lengths, (2, 2, 1), dk, dv, io, seed=68, state=True, sd=torch.bfloat16))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("B,T,heads", [(3, 90, (4, 2, 4)), (5, 1, (2, 2, 2)), (2, 700, (2, 1, 1)), (4, 64, (1, 3, 3))])
+def test_backward_of_dense_batches(B, T, heads, state, io):
+    """[B,T,H,D] rows without cu_seqlens, and the same with it: bit for bit."""
+    from mamba_selective_ssm_ssd_amd import linear
+    c = Case([T] * B, heads, 64, 32, io, seed=69, state=state)
+    dense = [t.view(B, T, *t.shape[1:]) for t in (c.q, c.k, c.v, c.go)]
+    g = linear.backward(*dense[:3], c.ld, dense[3], state=c.state, gfinal=c.gfinal)
+    assert all(g[n].shape == dense["qkv".index(n)].shape for n in "qkv")
+    flat = {n: t if n == "state" else t.flatten(0, 1) for n, t in g.items()}
+    _compare_backward(c, flat)
+    same = linear.backward(*c.args(), c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev, max_seqlen=T)
+    assert all(torch.equal(flat[n], same[n]) for n in same)

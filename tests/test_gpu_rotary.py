@@ -221,3 +221,30 @@ def test_norm_without_eps_and_sets_of_rows_in_part(T, hq, hk, D, rot, halves, ep
         size = r * gn * np.abs(w) + r ** 3 * a * np.mean(a * gn * np.abs(w), -1, keepdims=True)
         assert (np.abs(_np(got[n]) - dx) <= 64 * E * size + r16 * np.abs(dx)).all()
         assert (np.abs(_np(got[n + "_weight"]) - dw) <= 128 * E * np.sum(gn * a * r, axis=(0, 1))).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("halves", [False, True])
+def test_gradients_in_place(halves, norm, io):
+    """Through the C ABI: the gradients of q and k in the rows of gq and gk, and in the rows of q and k."""
+    from mamba_selective_ssm_ssd_amd import capi, rotary
+    T, hq, hk, D = 70, 5, 3, 96
+    q, k, pos, f, qw, kw = _setup(T, hq, hk, D, 64, io, weight=norm)
+    gq, gk = (torch.randn(x.shape, generator=torch.Generator().manual_seed(i)).to(DT[io]).cuda() for i, x in enumerate((q, k)))
+    want = rotary.norm_rotate_backward(q, k, pos, f, gq, gk, norm=norm, q_weight=qw, k_weight=kw, halves=halves)
+    shape = capi.m3_rotary_shape_t(T, hq, hk, D, 64, 1, capi.M3_DTYPE_BF16 if io == "bf16" else capi.M3_DTYPE_F32, 0, halves, norm, 1e-6)
+    ws = torch.empty(capi.m3_norm_rotate_backward_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
+    rows = lambda t: capi.m3_rows_t(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    for over in ("g", "x"):
+        x, g = [q.clone(), k.clone()], [gq.clone(), gk.clone()]
+        out = g if over == "g" else x
+        dw = [torch.empty(D, device="cuda") if norm else None for _ in range(2)]
+        rc = capi.m3_norm_rotate_backward(shape, rows(x[0]), rows(x[1]), pos.data_ptr(), f.data_ptr(),
+                                          *(t.data_ptr() if norm else None for t in (qw, kw)), rows(g[0]), rows(g[1]), rows(out[0]), rows(out[1]),
+                                          *(t.data_ptr() if norm else None for t in dw), ws.data_ptr(), ws.numel(),
+                                          torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want["q"]) and torch.equal(out[1], want["k"])
+        assert not norm or torch.equal(dw[0], want["q_weight"]) and torch.equal(dw[1], want["k_weight"])
