@@ -48,7 +48,8 @@ typedef struct {
 } m3_rotary_shape_t;
 
 /* positions [axes][tokens], inv_freq [axes][rot / 2] fp32; q_weight and
- * k_weight [dim] fp32 or NULL (they need norm). */
+ * k_weight [dim] fp32 or NULL (they need norm).  inv_freq and the weights start
+ * at multiples of 16 bytes. */
 m3_status_t m3_norm_rotate(const m3_rotary_shape_t *shape, const m3_rows_t *q, const m3_rows_t *k,
                            const void *positions, const float *inv_freq, const float *q_weight,
                            const float *k_weight, const m3_rows_t *q_out, const m3_rows_t *k_out,

@@ -1,7 +1,6 @@
 // k_linear.hpp -- linear attention with a decay for each head: the chunked
 // scan that serves the prompt pass and, with its operands exchanged or the
-// tokens walked backwards, the three gradients; the join of a cut sequence's
-// segment states; the sum of a shared row's gradients.
+// tokens walked backwards, the three gradients, and its launch.
 //
 // One scan, with g = exp(log_decay) and rows x_i, y_i (DX channels) and z_i
 // (DZ channels) in scan order, keeps a DX x DZ state S in fp32 and writes
@@ -27,8 +26,8 @@
 // Chunks of 64 rows: as many as two workgroups a compute unit have room for.
 //
 // Bound by memory where the chip is full, at 4.5 to 4.9 TB/s of the 5.2 that a
-// large copy reaches: 32 x 1024 x 32 x 128 235 us (4.6 TB/s); of 65536 x 64 x 64
-// cut into 64 segments the pre-pass 241 us (4.7) and the outputs 450 us (4.9).
+// large copy reaches: 32 x 1024 x 32 x 128 250 us (4.6 TB/s); of 65536 x 64 x 64
+// cut into 64 segments the pre-pass 238 us (4.7) and the outputs 450 us (4.9).
 // Matrix units are busy 23% of the time, LDS 25%, vector units 31%.  Few
 // workgroups are bound by the chain of chunks: 3.3 us per 64 rows of 128 x 128.
 #pragma once
@@ -86,7 +85,9 @@ constexpr int64_t kSlotSkip = -1, kSlotTaken = -2;
 
 // State of sequence b: its slot, kSlotSkip for padding, kSlotTaken where an
 // earlier sequence of the call names the same slot.  All threads of the
-// workgroup call it.
+// workgroup call it.  Every workgroup reads the slots before its own: prompts of
+// 4096 x 16 tokens of 16 x 64 x 64 934 us, 1126 with slots, and 496 and 568 of
+// 1024 x 32 of 32 x 64 x 64, most of it the states' order in memory.
 __device__ __forceinline__ int64_t lin_slot(const int32_t *slots, int64_t nstates, int64_t b) {
     if (!slots) return b;
     const int64_t s = slots[b];
@@ -200,7 +201,7 @@ struct LinCfg {
     // planes of the weights: a row of a few tokens is the sum of a few of them, so a
     // bf16 result would show one plane's rounding whole, beside its own
     static constexpr int WP = F32 ? 3 : 2;
-    static constexpr int Q = F32 || (OUT && DX == 128 && DZ == 128) ? 32 : 64; // 64 rows of 128 x 128 spill (442 us for 219)
+    static constexpr int Q = F32 || (OUT && DX == 128 && DZ == 128) ? 32 : 64; // 64 rows of 128 x 128 spill (gradients of 4999 x 32 (8) x 128 442 us for 219)
     static constexpr int MP = DX / 32, NP = DZ / 32; // 32 x 32 blocks of the state, 16 x 16 tiles in pairs
     // the state's tiles over the waves: MW along x (MTW tiles each, a pair of
     // one block where it is two), NW along z
@@ -609,7 +610,11 @@ __global__ __launch_bounds__((LinCfg<IO, DX, DZ, OUT>::T), (LinCfg<IO, DX, DZ, O
 #pragma unroll
             for (int j = 0; j < C::NTW; ++j) {
                 // a bf16 result takes the state rounded to bf16 as operand: one
-                // rounding per term, the size of the result's own
+                // rounding per term, the size of the result's own, and a relative
+                // error of 0.0022 where the result's rounding alone makes 0.0017.
+                // A second plane would make it that, but leaves one workgroup a unit
+                // at 128 x 128: 16 ragged sequences of 1024 x 32 x 128 207 -> 270 us,
+                // gradients of 4 x 2048 x 64 x 64 144 -> 158
                 uint16_t *const f = sf + (((mt0 >> 1) * NT + tile(j)) * 64 + lane) * 8;
                 float a[8];
 #pragma unroll

@@ -28,10 +28,11 @@ inline bool lin_spread(int64_t segments, int32_t heads, int32_t hg, int32_t tile
 //
 // Heads that share rows, and more neighbours of them: their rows lie side by
 // side in memory.  Up to 16 where that leaves 32 groups an XCD to spread: 65536
-// x 64 x 64 takes 703 us, 780 with one; 16 ragged sequences of 32 heads of 128
-// 228 us with 16, 208 with one.  Several scans of whole sequences, which are of
+// x 64 x 64 takes 706 us, 769 with one; 16 ragged sequences of 32 heads of 128
+// 224 us with 16, 205 with one.  Several scans of whole sequences, which are of
 // like lengths, up to eight and two groups an XCD: gradients of 4 x 2048 x 64 x
-// 64 147 us, 161 with one; of cut ones 232, 217 with no more than share rows.
+// 64 148 us, 165 with one; of cut ones, 4999 x 32 (8) x 128, 225, 211 with no
+// more than share rows.
 // Fewer than share rows where groups of all of them would leave XCDs idle: 200
 // tokens of 64 heads of 128 that share one row of k and of v 13.9 us, 58 as one
 // group, its gradients 44 and 88; gradients of 1000 such tokens 89 and 282, of

@@ -18,7 +18,9 @@ namespace m3 {
 // blockIdx.x: (sequence, head), blockIdx.y: 1024 entries of the state,
 // blockIdx.z: scan.  A thread has four entries and eight segments' loads in
 // flight: bound by reading and writing the states (64 segments of 64 x 64 x 64
-// heads, 134 MB, 30 us: 4.5 TB/s), or by the chain of loads where they are few.
+// heads, 134 MB, 30 us: 4.5 TB/s), or by the chain of loads where they are few,
+// which goes through the segments one after another: two unlike sequences,
+// 8192 x 8 x 128 in all, in 32 segments, 12 us beside scans of 15 and 24.
 __global__ __launch_bounds__(256) void k_linear_join(const LinParams p) {
     const LinRole &R = p.role[blockIdx.z];
     const int64_t b = blockIdx.x / p.H, h = blockIdx.x % p.H;
@@ -97,7 +99,11 @@ __global__ __launch_bounds__(256) void k_linear_sum(const LinSums p) {
 // the first is used.  States are read and written past the caches, as the layers
 // between two steps leave nothing of them there:
 // 100 us (5.4 TB/s) against 111 us with reads alone and 114 us with neither, over
-// 256 x 64 fp32 states of 64 x 64 taken in turn from more than the cache holds.
+// 256 x 64 fp32 states of 64 x 64 taken in turn from more than the cache holds;
+// bf16 states, of which a lane loads 8 bytes, 63 us (4.3 TB/s).
+// With slots a workgroup also reads those before its own: as slots in order
+// nothing to 1024 sequences, 4% of 4096 x 16 states of 64 x 64, 40% of 16384 x 4
+// of them; in any order states lie apart, which costs 13% at 1024 x 64.
 // ---------------------------------------------------------------------------
 struct LinStepParams {
     const void *q, *k, *v;
@@ -292,6 +298,9 @@ int64_t segment(const m3_linear_shape_t *s, int scans, int columns) {
     // Enough workgroups for most compute units, none much longer than the others:
     // the chip is full without cutting, and nothing is read twice (8 x 2048 x 32 x
     // 128 144 us, 177 cut by 1024; gradients of 4 x 2048 x 32 x 128 184 us, 222 cut).
+    // It counts workgroups and not how long their chains are: gradients of one
+    // sequence of 65536 x 64 x 64, 192 workgroups, take 1570 us, twice the time of
+    // their bytes.
     if (longest <= 256 || (s->batch * per >= 192 && longest * s->batch < 2 * s->tokens)) return 0;
     // Else two workgroups a compute unit, all that fit at once: longer segments leave
     // some idle, shorter ones read and write states instead of rows (16 ragged

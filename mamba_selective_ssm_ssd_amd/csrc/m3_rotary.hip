@@ -182,8 +182,8 @@ __global__ __launch_bounds__(kRT) void k_norm_rotate(const RotParams p) {
 //     dw = sum gn r x,    dx = r w gn - (r^3 / dim) x sum(x w gn).
 // Workgroups are q's or k's, walk their items with a fixed stride and keep their
 // share of dw in registers; k_norm_rotate_sum adds the shares in a fixed order.
-// Bound by its rows: 8192 x 128 x 64 in bf16 73 us (5.5 TB/s), 3001 x 20 x 96 in
-// fp32 17.5 us (4.0 TB/s).
+// Bound by its rows: 8192 x 128 x 64 in bf16 73 us (5.5 TB/s); where q and k have
+// unlike head counts, by the share of workgroups that each gets (backward_grid).
 template <typename IO, int LPR, bool HALVES>
 __global__ __launch_bounds__(kRT, 4) void k_norm_rotate_backward(const RotParams p) {
     constexpr int RPW = 64 / LPR, NW = kRT / 64;
@@ -302,8 +302,8 @@ hipError_t launch_rotary(RotParams &p, int64_t grid, bool back, hipStream_t s) {
     }
     // Below two waves a SIMD, or where a set holds all heads, a wave takes one set:
     // 512 x 40 x 128 4.8 us (5.4 with up to four sets), 32768 x 10 x 64 33 us (37).
-    // Else its angles serve up to four: 16384 x 40 x 128 57 us (5.9 TB/s; 79 with
-    // one, 60 with six), 1024 x 40 x 128 7.5 us (8.5 with one).
+    // Else its angles serve up to four: 16384 x 40 x 128 57 us a call, 54 the kernel
+    // (calls of 79 with one, 60 with six), 1024 x 40 x 128 7.5 us (8.5 with one).
     if (grid < 512 || std::max(p.r[0].heads, p.r[1].heads) <= 64 / LPR) {
         for (RotRows &r : p.r) r.items = (r.heads + 64 / LPR - 1) / (64 / LPR);
         grid = (p.tokens * (p.r[0].items + p.r[1].items) + 3) / 4;
@@ -389,8 +389,12 @@ bool rows_overlap(const m3_rotary_shape_t *s, const m3_rows_t *q, const m3_rows_
 
 // Workgroups of the gradients, for q and for k, in the ratio of their items: at
 // most the four per compute unit that are resident at once (128 registers), so
-// that they share the rows evenly and leave few partial sums.  Twice as many took
-// as long (76 us at 8192 x 128 x 64) and their sum 1 us more.
+// that they leave few partial sums.  Twice as many took as long (a call of 75 us at
+// 8192 x 128 x 64) and their sum 1 us more.  An item holds one to four sets of
+// rows, so the rows are shared evenly where q and k have as many heads; of 16 and
+// 4 heads of 96 channels k gets half the workgroups for a fifth of the rows (3001
+// tokens in fp32 17.5 us, 4.0 TB/s), of 32 and 8 of 128 a third for a fifth (16384
+// in bf16 91 us, 5.5 TB/s).
 struct BackGrid {
     int64_t q, k;
 };

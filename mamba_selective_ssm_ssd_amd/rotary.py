@@ -8,7 +8,8 @@ q [T,Hq,D], k [T,Hk,D] (or [B,T,H,D]) in float32 or bfloat16, strided as in
 ``linear``; positions [T] or [axes,T], int32 or int64; inv_freq [n] or
 [axes,n] float32, which turns the first 2 n channels: the pairs (2i, 2i+1), or
 (i, i+n) with halves=True.  ``axes_table`` lays out the frequencies of several
-axes (time, height, width).  D and 2 n are multiples of 8, D up to 256.
+axes (time, height, width).  D and 2 n are multiples of 8, D up to 256;
+inv_freq and the weights are contiguous and start at multiples of 16 bytes.
 """
 from __future__ import annotations
 
