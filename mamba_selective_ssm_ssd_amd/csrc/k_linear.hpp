@@ -361,18 +361,21 @@ __device__ __forceinline__ float lin_power(float ld2, int n) { return n > 0 ? __
 // s g^n, rounded once.  A slow decay is taken as s + s (g^n - 1): g^n itself,
 // rounded to 24 bits, would err the same way in every chunk of a long sequence.
 // Of an infinite s that sum makes inf - inf: such a result is s again, an
-// infinity as the product is, or the NaN that it was.
+// infinity as the product is, or the NaN that it was.  A decay that is NaN makes
+// everything NaN.
 struct LinDecay {
     float f;
     uint32_t keep; // all of s, or nothing, to add
+    float poison;  // 0, or NaN where f is
     __device__ __forceinline__ LinDecay(float ld, double n) {
         const float x = n > 0 ? float(double(ld) * n) : 0.f;
         f = x > -0.5f ? expm1f(x) : expf(x);
         keep = x > -0.5f ? 0xffffffffu : 0u;
+        poison = f - f;
     }
     __device__ __forceinline__ float operator()(float s) const {
         const float r = fmaf(s, f, __uint_as_float(__float_as_uint(s) & keep));
-        return r != r ? s : r;
+        return r != r ? s + poison : r;
     }
 };
 

@@ -808,3 +808,25 @@ def test_backward_of_dense_batches(B, T, heads, state, io):
     _compare_backward(c, flat)
     same = linear.backward(*c.args(), c.go, state=c.state, gfinal=c.gfinal, cu_seqlens=c.cu_dev, max_seqlen=T)
     assert all(torch.equal(flat[n], same[n]) for n in same)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_a_decay_that_is_nan_shows(io):
+    """Heads whose log_decay is NaN have NaN for states and outputs, in the step,
+    and in whole, folded and joined prompts; the others do not."""
+    from mamba_selective_ssm_ssd_amd import linear
+    nan = torch.tensor([False, True, False], device="cuda")
+    c = Case([1] * 3, (3, 3, 3), 32, 40, io, seed=70, state=True)
+    c.ld[nan] = float("nan")
+    pool = c.state.clone()
+    o = linear.decode_step(*c.args(), pool)
+    assert torch.isnan(o[:, nan].float()).all() and torch.isfinite(o[:, ~nan].float()).all()
+    assert torch.isnan(pool[:, nan]).all() and torch.isfinite(pool[:, ~nan]).all()
+    for n in (100, 700, 2600):
+        c = Case([n], (3, 3, 3), 32, 40, io, seed=71, state=True)
+        c.ld[nan] = float("nan")
+        o, f = _run_prefill(c)
+        assert torch.isnan(f[:, nan]).all() and torch.isfinite(f[:, ~nan]).all()
+        assert torch.isnan(o[1:, nan].float()).all() and torch.isfinite(o[:, ~nan].float()).all()
+        g = _run_backward(c)
+        assert torch.isnan(g["state"][:, nan]).all() and all(torch.isfinite(g[x][:, ~nan].float()).all() for x in g)
